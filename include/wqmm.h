@@ -215,6 +215,78 @@ WQMM_API wqmm_status wqmm_matmul_no_alloc(const wqmm_tensor* x1, const wqmm_tens
                                           int64_t comm_turn, int64_t stream_mode, int64_t antiquant_group_size,
                                           const wqmm_tensor* output, wqmm_stream stream);
 
+/* ================================================================ token routing
+ *
+ * Tokens sorted by expert and back, around the experts' products (one wqmm or
+ * qmm call per expert on its rows), and rows sorted by adapter for lora_*.
+ * Each operator has a phase 1 of its own; route_run is the phase 2 of all.
+ * Tensors are contiguous, their data aligned to their elements (16-byte
+ * alignment of rows and pointers gives the full speed), and no output overlaps
+ * an input.  A "slot" is one (token, choice) pair: a position tensor is (T) --
+ * one choice per token -- or (T, K) or (b, s, K).  1 <= hidden <= 65535.
+ *
+ * route_sort_get_workspace_size -- the stable order of the slots by expert.
+ *  expert_ids   (T), (T, K) or (b, s, K) int32 or int64; an id outside
+ *               [0, num_experts) belongs to no expert here (a dropped slot, or
+ *               one of another rank).  T * K <= 2^31 - 1; 0 is allowed.
+ *  num_experts  1 .. 2048.
+ *  offsets      out, (num_experts + 1) int32: expert e has the sorted rows
+ *               offsets[e] .. offsets[e + 1] - 1.
+ *  source       out, (T * K) int32: the slot (token * K + choice) of every
+ *               sorted row, ascending within an expert; behind
+ *               offsets[num_experts] the slots of no expert, ascending.
+ *  position     out, int32 of the shape of expert_ids: the sorted row of every
+ *               slot, -1 for a slot of no expert.
+ */
+WQMM_API wqmm_status route_sort_get_workspace_size(const wqmm_tensor* expert_ids, int64_t num_experts,
+                                                   const wqmm_tensor* offsets, const wqmm_tensor* source,
+                                                   const wqmm_tensor* position, uint64_t* workspace_size,
+                                                   wqmm_executor** executor);
+
+/* route_dispatch_get_workspace_size -- output[position[t, j]] = x[t].
+ *  x         (T, hidden) or (b, s, hidden), any dtype of whole bytes (an int8 GEMM's
+ *            per-token scales go along as hidden = 1).
+ *  position  int32; the valid entries are distinct.  An entry outside
+ *            [0, rows) is skipped, so an output with fewer rows than slots
+ *            drops what lies behind its last row.
+ *  output    (rows, hidden), dtype of x; rows no entry names stay as they are.
+ * The gradient is route_combine without weights. */
+WQMM_API wqmm_status route_dispatch_get_workspace_size(const wqmm_tensor* x, const wqmm_tensor* position,
+                                                       const wqmm_tensor* output, uint64_t* workspace_size,
+                                                       wqmm_executor** executor);
+
+/* route_combine_get_workspace_size --
+ *     output[t] = x3[t] + sum_j weights[t, j] * x_sorted[position[t, j]]
+ * summed in 32 bits in ascending j, rounded once.  An entry outside [0, rows)
+ * adds nothing (its weight is not read); a token without any gets x3, or zeros.
+ *  x_sorted  (rows, hidden) float16, bfloat16 or float32.
+ *  weights   optional (NULL: all one), shape of position, float16, bfloat16 or float32.
+ *  x3        optional addend, shape and dtype of output.
+ *  output    (T, hidden) or (b, s, hidden), dtype of x_sorted. */
+WQMM_API wqmm_status route_combine_get_workspace_size(const wqmm_tensor* x_sorted, const wqmm_tensor* position,
+                                                      const wqmm_tensor* weights, const wqmm_tensor* x3,
+                                                      const wqmm_tensor* output, uint64_t* workspace_size,
+                                                      wqmm_executor** executor);
+
+/* route_combine_grad_get_workspace_size -- the gradient of route_combine for
+ * x_sorted and weights (x3's is grad itself; without weights x_sorted's is
+ * route_dispatch of grad):
+ *     grad_sorted[position[t, j]] = weights[t, j] * grad[t]
+ *     grad_weights[t, j]          = sum_h grad[t, h] * x_sorted[position[t, j], h]
+ * The valid entries of position are distinct; an entry outside [0, rows) gives
+ * grad_weights 0, and rows no entry names keep what grad_sorted holds.
+ *  grad (T, hidden) or (b, s, hidden) float16, bfloat16 or float32; x_sorted and
+ *  grad_sorted (rows, hidden) of its dtype; weights and grad_weights of position's
+ *  shape, float16, bfloat16 or float32, the same dtype. */
+WQMM_API wqmm_status route_combine_grad_get_workspace_size(const wqmm_tensor* grad, const wqmm_tensor* x_sorted,
+                                                           const wqmm_tensor* position, const wqmm_tensor* weights,
+                                                           const wqmm_tensor* grad_sorted,
+                                                           const wqmm_tensor* grad_weights,
+                                                           uint64_t* workspace_size, wqmm_executor** executor);
+
+/* route_run -- phase 2 of the four operators above.  Consumes the executor. */
+WQMM_API wqmm_status route_run(void* workspace, uint64_t workspace_size, wqmm_executor* executor, wqmm_stream stream);
+
 /* ================================================================ utilities */
 
 /* Release an executor that was never passed to a *_run call (NULL is ignored). */

@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 from typing import Optional, Sequence
 
@@ -51,6 +52,11 @@ class WqmmTensor(ctypes.Structure):
 _lock = threading.Lock()
 _lib = None
 
+# phase 1 of the operators with a shared phase 2: name, descriptors, then integers (and more descriptors)
+_PLANNED = [("route_sort_get_workspace_size", 1, 1), ("route_dispatch_get_workspace_size", 3, 0),
+            ("route_combine_get_workspace_size", 5, 0), ("route_combine_grad_get_workspace_size", 6, 0)]
+_TENSORS_AFTER = {"route_sort_get_workspace_size": 3}
+
 
 def build(force: bool = False) -> str:
     """Compile libwqmm.so in-tree (nvcc, sm_100a)."""
@@ -85,6 +91,14 @@ def lib():
             L.wqmm_version.restype = ctypes.c_char_p
             L.qmm_debug_set_raw_accumulator.argtypes = [P, P]
             L.wqmm_debug_set_flag_wait.argtypes = [P, ctypes.c_uint64, I32]
+            # the routing and adapter operators: every descriptor a pointer to the struct's bytes
+            for name, tensors, ints in _PLANNED:
+                getattr(L, name).argtypes = [P] * tensors + [I64] * ints + [P] * (_TENSORS_AFTER.get(name, 0)) + [
+                    U64P, EXP]
+                getattr(L, name).restype = I32
+            for name in ("route_run",):
+                getattr(L, name).argtypes = [P, ctypes.c_uint64, P, P]
+                getattr(L, name).restype = I32
             for name in ("wqmm_get_workspace_size", "wqmm_run", "qmm_get_workspace_size", "qmm_run",
                          "wqmm_pack_weight_size", "wqmm_pack_weight", "wqmm_stream_wait", "wqmm_device_error",
                          "qmm_debug_set_raw_accumulator", "wqmm_debug_set_flag_wait"):
@@ -239,6 +253,36 @@ def wqmm_matmul_no_alloc(x1, x2, bias, antiquant_scale, antiquant_offset, x3, gr
              int(comm_turn), int(stream_mode), int(antiquant_group_size), _ref(output), _stream_handle(stream))
 
 
+def _phase1(name: str, *args):
+    """Phase 1 of an operator by its C name: descriptors as WqmmTensor or None."""
+    ws = ctypes.c_uint64(0)
+    ex = ctypes.c_void_p(None)
+    st = getattr(lib(), name)(*(_ref(a) if a is None or isinstance(a, WqmmTensor) else a for a in args),
+                              ctypes.byref(ws), ctypes.byref(ex))
+    return st, ws.value, ex.value
+
+
+def route_sort_get_workspace_size(expert_ids, num_experts, offsets, source, position):
+    return _phase1("route_sort_get_workspace_size", expert_ids, int(num_experts), offsets, source, position)
+
+
+def route_dispatch_get_workspace_size(x, position, output):
+    return _phase1("route_dispatch_get_workspace_size", x, position, output)
+
+
+def route_combine_get_workspace_size(x_sorted, position, weights, x3, output):
+    return _phase1("route_combine_get_workspace_size", x_sorted, position, weights, x3, output)
+
+
+def route_combine_grad_get_workspace_size(grad, x_sorted, position, weights, grad_sorted, grad_weights):
+    return _phase1("route_combine_grad_get_workspace_size", grad, x_sorted, position, weights, grad_sorted,
+                   grad_weights)
+
+
+def route_run(workspace: int, workspace_size: int, executor, stream=None) -> int:
+    return lib().route_run(workspace or None, workspace_size, executor, _stream_handle(stream))
+
+
 def check(status: int) -> None:
     if status != SUCCESS:
         raise WqmmError(status, wqmm_last_error())
@@ -277,6 +321,78 @@ def _workspace(nbytes: int, device):
         return None, 0
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return ws, ws.data_ptr()
+
+
+# ---------------------------------------------------------------- both phases of an operator on torch tensors
+_DESC_STRUCT = struct.Struct("=Qii3q3qii")  # wqmm_tensor, byte for byte
+_torch_codes: dict = {}
+
+
+def _desc_bytes(t) -> Optional[bytes]:
+    """The descriptor of a torch tensor as the struct's bytes (cheaper to make than a WqmmTensor: a call at a
+    few tokens is bound by the host)."""
+    if t is None:
+        return None
+    code = _torch_codes.get(t.dtype)
+    if code is None:
+        code = _torch_codes[t.dtype] = _torch_dtype_code(t)
+    shape, stride = t.shape, t.stride()
+    nd = len(shape)
+    if nd == 2:
+        return _DESC_STRUCT.pack(t.data_ptr(), code, 2, shape[0], shape[1], 0, stride[0], stride[1], 0, 0, 0)
+    if nd == 1:
+        return _DESC_STRUCT.pack(t.data_ptr(), code, 1, shape[0], 0, 0, stride[0], 0, 0, 0, 0)
+    if nd == 3:
+        return _DESC_STRUCT.pack(t.data_ptr(), code, 3, *shape, *stride, 0, 0)
+    raise ValueError(f"a tensor of 1 to 3 dimensions is expected, got {nd}")
+
+
+def _same_device(*tensors) -> int:
+    """The CUDA device index that all given tensors share."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("every tensor must be a CUDA tensor")
+            if dev is None:
+                dev = d
+            elif d != dev:
+                raise ValueError(f"tensors of two devices, {dev} and {d}: one device is expected")
+    return dev
+
+
+def _placed(device: int, stream):
+    """The context in which an operator on `device` allocates and launches: its device current, and `stream`
+    (a torch.cuda.Stream, a raw handle or None) too, so that what the call allocates belongs to that stream.
+    None where nothing has to change."""
+    import torch
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        elif stream.device_index != device:
+            raise ValueError(f"the stream is on device {stream.device_index}, the tensors on {device}")
+        return torch.cuda.stream(stream)  # makes its device current too
+    return None if torch.cuda.current_device() == device else torch.cuda.device(device)
+
+
+def _both_phases(phase1, run, device: int, *args) -> None:
+    """Phase 1 on descriptor bytes, the workspace, and phase 2 on the current stream of `device`."""
+    import torch
+    ws, ex = ctypes.c_uint64(0), ctypes.c_void_p(None)
+    st = phase1(*args, ctypes.byref(ws), ctypes.byref(ex))
+    if st:
+        check(st)
+    size, space = ws.value, None
+    if size:
+        try:
+            space = torch.empty(size, dtype=torch.uint8, device=device)
+        except BaseException:
+            wqmm_executor_destroy(ex)
+            raise
+    st = run(space.data_ptr() if size else None, size, ex, torch.cuda.current_stream(device).cuda_stream)
+    if st:
+        check(st)
 
 
 def weight_quant_matmul(x1, x2_desc: WqmmTensor, antiquant_scale, antiquant_offset=None, bias=None, x3=None,

@@ -10,6 +10,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <map>
+#include <memory>
 #include <mutex>
 #include <tuple>
 #include <new>
@@ -22,6 +23,7 @@
 #include <unistd.h>
 
 #include "../../include/wqmm.h"
+#include "host.h"
 #include "internal.h"
 
 using namespace wqmm;
@@ -33,6 +35,10 @@ thread_local uint64_t g_plan_ws_cap = 0;
 namespace {
 
 thread_local std::string g_last_error;
+
+}  // namespace
+
+namespace wqmm {
 
 wqmm_status fail(wqmm_status code, const char* fmt, ...) {
   char buf[512];
@@ -49,11 +55,13 @@ wqmm_status ok() {
   return WQMM_SUCCESS;
 }
 
+}  // namespace wqmm
+
+namespace {
+
 constexpr uint64_t kFlagWaitNs = 2000000000ull;  // a split tile's flag wait gives up after 2 s
 constexpr uint32_t kMagicLive = 0x57514D4Du;  // "WQMM"
 constexpr uint32_t kMagicDead = 0xDEADBEEFu;
-
-enum class OpKind { kWqmm, kQmm };
 
 struct Region {
   uint64_t offset = 0, bytes = 0;
@@ -107,6 +115,8 @@ struct wqmm_executor {
   // and whether its first owner waits for a value no owner writes
   uint64_t debug_wait_ns = 0;
   bool debug_flag_mismatch = false;
+  // operators whose plan lives outside this file
+  std::unique_ptr<OpPlan> plan;
 };
 
 namespace {
@@ -128,7 +138,11 @@ bool is_live(const wqmm_executor* ex) {
   return g_live.count(ex) != 0;
 }
 
+}  // namespace
+
 // ------------------------------------------------------------------ tensor helpers
+namespace wqmm {
+
 int64_t numel(const wqmm_tensor* t) {
   int64_t n = 1;
   for (int i = 0; i < t->ndim; ++i) n *= t->shape[i];
@@ -146,19 +160,6 @@ bool contiguous(const wqmm_tensor* t) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool act_dtype_ok(int dt) { return dt == WQMM_DT_F16 || dt == WQMM_DT_BF16; }
-
-// The anti-quant GEMM's weight kind for an x2 dtype (float16 / bfloat16: the
-// non-quantised scenario, x2 of the x1 dtype).
-int weight_kind(int x2_dtype) {
-  switch (x2_dtype) {
-    case WQMM_DT_I4: return kW4;
-    case WQMM_DT_I8: return kW8;
-    case WQMM_DT_FP8E4M3: return kWFp8;
-    default: return kWH;
-  }
-}
 
 const char* dt_name(int dt) {
   switch (dt) {
@@ -185,23 +186,6 @@ wqmm_status check_descriptor(const wqmm_tensor* t, const char* name) {
   return WQMM_SUCCESS;
 }
 
-// A value no earlier launch has written into a stream-K flag: a process-wide
-// counter (odd values, step 2) started at a value mixed from the clocks and the
-// process id, so that flags left in reused memory (by this or an earlier
-// process) do not match.
-uint64_t next_launch_token() {
-  static std::atomic<uint64_t> counter{[] {
-    uint64_t x = static_cast<uint64_t>(std::chrono::steady_clock::now().time_since_epoch().count());
-    x ^= static_cast<uint64_t>(std::chrono::system_clock::now().time_since_epoch().count()) << 21;
-    x ^= static_cast<uint64_t>(getpid()) << 40;
-    x ^= x >> 33;
-    x *= 0xff51afd7ed558ccdULL;
-    x ^= x >> 33;
-    return x | 1ULL;
-  }()};
-  return counter.fetch_add(2, std::memory_order_relaxed);  // odd, never zero, never repeated
-}
-
 int sm_count() {
   static std::once_flag once;
   static int sms = 148;
@@ -218,6 +202,44 @@ int sm_count() {
 }
 
 uint64_t round_up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
+
+wqmm_status cuda_fail(cudaError_t e, const char* what) {
+  return fail(WQMM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+}  // namespace wqmm
+
+namespace {
+
+bool act_dtype_ok(int dt) { return dt == WQMM_DT_F16 || dt == WQMM_DT_BF16; }
+
+// The anti-quant GEMM's weight kind for an x2 dtype (float16 / bfloat16: the
+// non-quantised scenario, x2 of the x1 dtype).
+int weight_kind(int x2_dtype) {
+  switch (x2_dtype) {
+    case WQMM_DT_I4: return kW4;
+    case WQMM_DT_I8: return kW8;
+    case WQMM_DT_FP8E4M3: return kWFp8;
+    default: return kWH;
+  }
+}
+
+// A value no earlier launch has written into a stream-K flag: a process-wide
+// counter (odd values, step 2) started at a value mixed from the clocks and the
+// process id, so that flags left in reused memory (by this or an earlier
+// process) do not match.
+uint64_t next_launch_token() {
+  static std::atomic<uint64_t> counter{[] {
+    uint64_t x = static_cast<uint64_t>(std::chrono::steady_clock::now().time_since_epoch().count());
+    x ^= static_cast<uint64_t>(std::chrono::system_clock::now().time_since_epoch().count()) << 21;
+    x ^= static_cast<uint64_t>(getpid()) << 40;
+    x ^= x >> 33;
+    x *= 0xff51afd7ed558ccdULL;
+    x ^= x >> 33;
+    return x | 1ULL;
+  }()};
+  return counter.fetch_add(2, std::memory_order_relaxed);  // odd, never zero, never repeated
+}
 
 // Resident CTA pairs of the pair-mode int8 GEMM per (device, output type).
 int qmm_pair_slots_cached(bool out_bf16) {
@@ -799,10 +821,6 @@ wqmm_status make_tmap(CUtensorMap* map, const void* base, CUtensorMapDataType dt
   return WQMM_SUCCESS;
 }
 
-wqmm_status cuda_fail(cudaError_t e, const char* what) {
-  return fail(WQMM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
 wqmm_status take_executor(wqmm_executor* ex, OpKind op) {
   if (!ex) return fail(WQMM_ERR_EXECUTOR, "executor is null");
   if (!is_live(ex) || ex->magic != kMagicLive)
@@ -1031,6 +1049,33 @@ extern "C" wqmm_status qmm_run(void* workspace, uint64_t workspace_size, wqmm_ex
   release(executor);
   return st == WQMM_SUCCESS ? ok() : st;
 }
+
+// ===================================================================== executors of the other operators
+namespace wqmm {
+
+wqmm_status hand_out(OpKind op, std::unique_ptr<OpPlan> plan, uint64_t workspace, uint64_t* workspace_size,
+                     wqmm_executor** executor) {
+  std::unique_ptr<wqmm_executor> ex(new wqmm_executor());
+  ex->op = op;
+  ex->workspace = workspace;
+  ex->plan = std::move(plan);
+  register_executor(ex.get());
+  *workspace_size = workspace;
+  *executor = ex.release();
+  return ok();
+}
+
+wqmm_status run_plan(OpKind op, void* workspace, uint64_t workspace_size, wqmm_executor* executor,
+                     wqmm_stream stream) {
+  wqmm_status st = take_executor(executor, op);
+  if (st) return st;
+  st = check_workspace(executor, workspace, workspace_size);
+  if (st == WQMM_SUCCESS) st = executor->plan->run(workspace, reinterpret_cast<cudaStream_t>(stream));
+  release(executor);
+  return st == WQMM_SUCCESS ? ok() : st;
+}
+
+}  // namespace wqmm
 
 // ===================================================================== weight packing
 namespace {

@@ -1,0 +1,52 @@
+// launch.cuh -- launches of the routing and adapter kernels: a chain of short
+// kernels on one stream, each launched while the one before it still runs
+// (programmatic stream serialisation), so that a launch's latency is not paid
+// after every kernel of an operator.
+//
+// Every thread of every such kernel calls pdl_wait() before its first access
+// to global memory: it returns when the preceding grid has finished and its
+// writes are visible, so nothing else about stream order changes.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <utility>
+
+namespace wqmm {
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next grid of the stream start its CTAs once every CTA of this one
+// has called it (or ended); they wait in pdl_wait().
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// `cluster`: CTAs of a cluster along grid.x (1: none).
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t s,
+                       A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+// The kernel's dynamic shared memory limit on the current device, raised once
+// per device and kernel (`done` is that kernel's bit mask of devices).
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+}
+
+}  // namespace wqmm
