@@ -287,6 +287,49 @@ WQMM_API wqmm_status route_combine_grad_get_workspace_size(const wqmm_tensor* gr
 /* route_run -- phase 2 of the four operators above.  Consumes the executor. */
 WQMM_API wqmm_status route_run(void* workspace, uint64_t workspace_size, wqmm_executor* executor, wqmm_stream stream);
 
+/* ================================================================ low-rank adapters
+ *
+ * lora_get_workspace_size -- low-rank adapters of many requests beside a shared
+ * projection, typically a wqmm or qmm output:
+ *     output[r] = y[r] + scale[a] * (x1[r] @ lora_a[a]^T) @ lora_b[a]^T,  a the adapter of row r
+ *  x1       (m, k) or (b, s, k) float16 or bfloat16.
+ *  lora_a   (adapters, rank, k), lora_b (adapters, n, rank): contiguous, dtype of x1.
+ *           1 <= adapters <= 2048; rank a multiple of 8 in [8, 128] (pad a smaller one with zeros).
+ *  scale    optional (adapters) float32 (NULL: all one).
+ *  offsets, source  the rows in the order of their adapters, as route_sort
+ *           makes them of one adapter index per row: (adapters + 1) and (m)
+ *           int32.  Rows of no adapter (index outside [0, adapters)) get y, or zeros.
+ *  y        optional addend, shape of output; may be the output itself (in place).
+ *  output   (m, n) or (b, s, n), dtype of x1.
+ * x1, y and output may have any row stride that is a multiple of 8 elements (a
+ * slice of a fused projection); every pointer to 16-bit data is 16-byte
+ * aligned.  k and n are multiples of 32 in [32, 65535].  Sums are held in 32
+ * bits, x1 @ lora_a^T to at least 16 bits of its value, and the result is rounded once. */
+WQMM_API wqmm_status lora_get_workspace_size(const wqmm_tensor* x1, const wqmm_tensor* lora_a,
+                                             const wqmm_tensor* lora_b, const wqmm_tensor* scale,
+                                             const wqmm_tensor* offsets, const wqmm_tensor* source,
+                                             const wqmm_tensor* y, const wqmm_tensor* output,
+                                             uint64_t* workspace_size, wqmm_executor** executor);
+
+/* lora_grad_get_workspace_size -- its gradient, given grad of the output (y's is grad itself):
+ *     grad_x[r] = grad_x_in[r] + scale[a] * (grad[r] @ lora_b[a]) @ lora_a[a]
+ *     grad_a[a] = scale[a] * sum_r (grad[r] @ lora_b[a])^T x1[r]
+ *     grad_b[a] = scale[a] * sum_r grad[r]^T (x1[r] @ lora_a[a]^T)     over the rows r of adapter a
+ *  grad       (m, n) or (b, s, n); grad_x optional (NULL: not wanted) and
+ *  grad_x_in  optional addend (the projection's own part; may be grad_x itself),
+ *             (m, k) or (b, s, k), all of x1's dtype, row strides as above.
+ *  grad_a, grad_b  contiguous, shape and dtype of lora_a and lora_b; zeros for an adapter without rows. */
+WQMM_API wqmm_status lora_grad_get_workspace_size(const wqmm_tensor* grad, const wqmm_tensor* x1,
+                                                  const wqmm_tensor* lora_a, const wqmm_tensor* lora_b,
+                                                  const wqmm_tensor* scale, const wqmm_tensor* offsets,
+                                                  const wqmm_tensor* source, const wqmm_tensor* grad_x_in,
+                                                  const wqmm_tensor* grad_x, const wqmm_tensor* grad_a,
+                                                  const wqmm_tensor* grad_b, uint64_t* workspace_size,
+                                                  wqmm_executor** executor);
+
+/* lora_run -- phase 2 of both.  Consumes the executor. */
+WQMM_API wqmm_status lora_run(void* workspace, uint64_t workspace_size, wqmm_executor* executor, wqmm_stream stream);
+
 /* ================================================================ utilities */
 
 /* Release an executor that was never passed to a *_run call (NULL is ignored). */

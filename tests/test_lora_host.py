@@ -1,0 +1,130 @@
+"""Low-rank adapters without a GPU: what phase 1 refuses and accepts, workspace sizes, executors, and the checks of the
+torch wrappers."""
+import pytest
+
+import weight_quantized_gemm_anti_b200 as W
+from weight_quantized_gemm_anti_b200 import lora
+from weight_quantized_gemm_anti_b200.routing import TokenOrder
+
+FAKE = 0x10000  # never dereferenced: phase 1 reads descriptors only
+NULL, INVALID = W.ERR_PARAM_NULLPTR, W.ERR_PARAM_INVALID
+F16, BF16, F32, I32 = W.DT_F16, W.DT_BF16, W.DT_F32, W.DT_I32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    W.build()
+
+
+def T(shape, dtype, strides=None, data=FAKE, fmt=W.FORMAT_ND):
+    return W.desc(data=data, dtype=dtype, shape=shape, strides=strides, fmt=fmt)
+
+
+def call(f, *args):
+    st, ws, ex = f(*(None if a is None else T(*a[:2], **(a[2] if len(a) > 2 else {})) for a in args))
+    if ex:
+        W.wqmm_executor_destroy(ex)
+    return st, ws
+
+
+ADD = dict(x1=((6, 64), BF16), a=((3, 16, 64), BF16), b=((3, 96, 16), BF16), scale=((3,), F32), offsets=((4,), I32),
+           source=((6,), I32), y=((6, 96), BF16), out=((6, 96), BF16))
+
+
+def add(**kw):
+    t = {**ADD, **kw}
+    return call(W.lora_get_workspace_size, t["x1"], t["a"], t["b"], t["scale"], t["offsets"], t["source"], t["y"],
+                t["out"])
+
+
+def test_add_accepts():
+    st, ws = add()
+    assert st == 0 and ws >= 6 * 2 * 16 * 2
+    assert add(y=None)[0] == 0 and add(scale=None)[0] == 0
+    assert add(x1=((2, 3, 64), BF16), y=((2, 3, 96), BF16), out=((6, 96), BF16))[0] == 0
+    # slices of wider matrices; three dimensions whose rows are at one stride
+    assert add(x1=((6, 64), BF16, dict(strides=(200, 1))), y=None,
+               out=((6, 96), BF16, dict(strides=(288, 1))))[0] == 0
+    assert add(x1=((2, 3, 64), BF16, dict(strides=(600, 200, 1))))[0] == 0
+    assert add(x1=((6, 1, 64), BF16, dict(strides=(72, 1, 1))))[0] == 0
+    assert add(x1=((1, 6, 64), BF16, dict(strides=(8, 72, 1))))[0] == 0
+    for rank in (8, 24, 128):
+        assert add(a=((3, rank, 64), BF16), b=((3, 96, rank), BF16))[0] == 0
+    one = dict(x1=((1, 64), F16, dict(strides=(3, 1))), a=((3, 16, 64), F16), b=((3, 96, 16), F16), source=((1,), I32),
+               y=None, out=((1, 96), F16))
+    assert add(**one)[0] == 0  # a single row has no stride
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x1=((6, 64), F32)), dict(x1=((6, 64), F16)), dict(x1=((0, 64), BF16)), dict(x1=((64,), BF16)),
+    dict(x1=((6, 48), BF16), a=((3, 16, 48), BF16)), dict(x1=((6, 64), BF16, dict(strides=(68, 1)))),
+    dict(x1=((6, 64), BF16, dict(strides=(56, 1)))), dict(x1=((6, 64), BF16, dict(strides=(-64, 1)))),
+    dict(x1=((6, 64), BF16, dict(strides=(1, 6)))), dict(x1=((2, 3, 64), BF16, dict(strides=(640, 200, 1)))),
+    dict(x1=((6, 64), BF16, dict(strides=(2 ** 32, 1)))), dict(x1=((6, 64), BF16, dict(data=FAKE + 8))),
+    dict(x1=((2 ** 31 - 1, 2 ** 31 - 1, 64), BF16)), dict(x1=((6, 64), BF16, dict(fmt=W.FORMAT_PACKED))),
+    dict(a=((3, 16, 96), BF16)), dict(a=((3, 12, 64), BF16), b=((3, 96, 12), BF16)),
+    dict(a=((3, 136, 64), BF16), b=((3, 96, 136), BF16)), dict(a=((3, 0, 64), BF16), b=((3, 96, 0), BF16)),
+    dict(a=((16, 64), BF16)), dict(a=((3, 16, 64), BF16, dict(strides=(2048, 64, 1)))),
+    dict(a=((2049, 16, 64), BF16), b=((2049, 96, 16), BF16), scale=None, offsets=((2050,), I32)),
+    dict(b=((2, 96, 16), BF16)), dict(b=((3, 96, 8), BF16)), dict(b=((3, 80, 16), BF16), y=None, out=((6, 80), BF16)),
+    dict(b=((3, 96, 16), BF16, dict(data=FAKE + 2))), dict(scale=((2,), F32)), dict(scale=((3,), BF16)),
+    dict(offsets=((3,), I32)), dict(offsets=((4,), W.DT_I64)), dict(source=((5,), I32)),
+    dict(source=((6, 1), I32)), dict(y=((6, 64), BF16)), dict(y=((5, 96), BF16)), dict(y=((6, 96), F16)),
+    dict(out=((6, 64), BF16)), dict(out=((6, 96), F32)), dict(y=((6, 96), BF16), out=((6, 96), BF16, dict(strides=(104, 1))))])
+def test_add_refuses(kw):
+    assert add(**kw)[0] == INVALID
+    assert W.wqmm_last_error()
+
+
+GRAD = dict(grad=((6, 96), BF16), x1=((6, 64), BF16), a=((3, 16, 64), BF16), b=((3, 96, 16), BF16), scale=((3,), F32),
+            offsets=((4,), I32), source=((6,), I32), gx_in=((6, 64), BF16), gx=((6, 64), BF16),
+            ga=((3, 16, 64), BF16), gb=((3, 96, 16), BF16))
+
+
+def grad(**kw):
+    t = {**GRAD, **kw}
+    return call(W.lora_grad_get_workspace_size, *(t[n] for n in GRAD))
+
+
+def test_grad_arguments():
+    st, ws = grad()
+    assert st == 0 and ws >= 2 * 6 * 2 * 16 * 2
+    assert grad(gx_in=None)[0] == 0 and grad(gx_in=None, gx=None)[0] == 0 and grad(scale=None)[0] == 0
+    assert grad(gx=None)[0] == NULL  # an addend without a result
+    for name in ("grad", "x1", "a", "b", "offsets", "source", "ga", "gb"):
+        assert grad(**{name: None})[0] == NULL, name
+    for kw in (dict(grad=((6, 64), BF16)), dict(grad=((6, 96), F16)), dict(gx=((6, 96), BF16)),
+               dict(gx_in=((5, 64), BF16)), dict(ga=((3, 64, 16), BF16)), dict(ga=((3, 16, 64), F32)),
+               dict(gb=((3, 96, 16), BF16, dict(strides=(1600, 16, 1)))), dict(gb=((96, 16), BF16)),
+               dict(gx=((6, 64), BF16, dict(strides=(72, 1)))),
+               dict(ga=((2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1), BF16))):
+        assert grad(**kw)[0] == INVALID, kw
+
+
+def test_null_pointers():
+    for name in ("x1", "a", "b", "offsets", "source", "out"):
+        assert add(**{name: None})[0] == NULL, name
+        shape, dtype = ADD[name][:2]
+        assert add(**{name: (shape, dtype, dict(data=0))}, **({} if name != "out" else dict(y=None)))[0] == NULL, name
+
+
+def test_executors_are_one_shot_and_of_their_own_kind():
+    t = ADD
+    args = [T(*t[n]) for n in ("x1", "a", "b", "scale", "offsets", "source", "y", "out")]
+    st, ws, ex = W.lora_get_workspace_size(*args)
+    assert st == 0
+    assert W.route_run(0, 0, ex, 0) == W.ERR_EXECUTOR
+    assert W.lora_run(0, ws, ex, 0) == W.ERR_WORKSPACE  # a workspace is needed: refused, and consumed
+    assert W.lora_run(FAKE, ws, ex, 0) == W.ERR_EXECUTOR
+
+
+def test_wrappers_refuse():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(6, 64, dtype=torch.bfloat16)
+    a, b = torch.zeros(3, 16, 64, dtype=torch.bfloat16), torch.zeros(3, 96, 16, dtype=torch.bfloat16)
+    order = TokenOrder(torch.zeros(4, dtype=torch.int32), torch.zeros(6, dtype=torch.int32), None)
+    for f in (lambda: lora.lora_add(x, a, b, order), lambda: lora.adapter_order(torch.zeros(6, dtype=torch.int32), 3),
+              lambda: lora.lora_grad(torch.zeros(6, 96), x, a, b, order),
+              lambda: lora.lora_weight_quant_matmul(x, W.desc(a[0]), None, a, b, order)):
+        with pytest.raises(ValueError, match="CUDA"):
+            f()

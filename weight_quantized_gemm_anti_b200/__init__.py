@@ -54,7 +54,8 @@ _lib = None
 
 # phase 1 of the operators with a shared phase 2: name, descriptors, then integers (and more descriptors)
 _PLANNED = [("route_sort_get_workspace_size", 1, 1), ("route_dispatch_get_workspace_size", 3, 0),
-            ("route_combine_get_workspace_size", 5, 0), ("route_combine_grad_get_workspace_size", 6, 0)]
+            ("route_combine_get_workspace_size", 5, 0), ("route_combine_grad_get_workspace_size", 6, 0),
+            ("lora_get_workspace_size", 8, 0), ("lora_grad_get_workspace_size", 11, 0)]
 _TENSORS_AFTER = {"route_sort_get_workspace_size": 3}
 
 
@@ -96,7 +97,7 @@ def lib():
                 getattr(L, name).argtypes = [P] * tensors + [I64] * ints + [P] * (_TENSORS_AFTER.get(name, 0)) + [
                     U64P, EXP]
                 getattr(L, name).restype = I32
-            for name in ("route_run",):
+            for name in ("route_run", "lora_run"):
                 getattr(L, name).argtypes = [P, ctypes.c_uint64, P, P]
                 getattr(L, name).restype = I32
             for name in ("wqmm_get_workspace_size", "wqmm_run", "qmm_get_workspace_size", "qmm_run",
@@ -281,6 +282,19 @@ def route_combine_grad_get_workspace_size(grad, x_sorted, position, weights, gra
 
 def route_run(workspace: int, workspace_size: int, executor, stream=None) -> int:
     return lib().route_run(workspace or None, workspace_size, executor, _stream_handle(stream))
+
+
+def lora_get_workspace_size(x1, lora_a, lora_b, scale, offsets, source, y, output):
+    return _phase1("lora_get_workspace_size", x1, lora_a, lora_b, scale, offsets, source, y, output)
+
+
+def lora_grad_get_workspace_size(grad, x1, lora_a, lora_b, scale, offsets, source, grad_x_in, grad_x, grad_a, grad_b):
+    return _phase1("lora_grad_get_workspace_size", grad, x1, lora_a, lora_b, scale, offsets, source, grad_x_in, grad_x,
+                   grad_a, grad_b)
+
+
+def lora_run(workspace: int, workspace_size: int, executor, stream=None) -> int:
+    return lib().lora_run(workspace or None, workspace_size, executor, _stream_handle(stream))
 
 
 def check(status: int) -> None:

@@ -447,8 +447,7 @@ cudaError_t sort_as(const SortParams& p, cudaStream_t s) {
   }
   while (place_smem(threads / 32, p.groups) > 200 * 1024) threads = (threads / 2 + 31) & ~31;
   const size_t smem = place_smem(threads / 32, p.groups);
-  const cudaError_t e = allow_smem(sort_place_kernel<IdT>, 200 * 1024);
-  if (e != cudaSuccess) return e;
+  if (const cudaError_t e = allow_smem(sort_place_kernel<IdT>, smem); e != cudaSuccess) return e;
   return launch_pdl(sort_place_kernel<IdT>, dim3(p.chunks), dim3(threads), smem, 1, s, p);
 }
 

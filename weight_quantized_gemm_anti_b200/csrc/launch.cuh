@@ -42,10 +42,10 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-// The kernel's dynamic shared memory limit on the current device, raised once
-// per device and kernel (`done` is that kernel's bit mask of devices).
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device (48 KB need no asking).
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
 

@@ -1,0 +1,183 @@
+// lora_common.cuh -- what the kernels of the low-rank adapters share.  Low-rank adapters of
+// many requests beside a shared projection, and their gradients:
+//
+//   forward   low = s x A^T          (shrink: contraction over k)
+//             out = y + low B^T      (expand: contraction over the rank)
+//   backward  back = s g B           (shrink over n),  low again from x
+//             dx = dx0 + back A      (expand)
+//             dA = back^T x, dB = g^T low   (outer: contraction over the rows)
+//
+// with A, B and s those of the row's adapter.  The rows are read in the order
+// of their adapters (`source`), so that a tile of rows shares one adapter.
+//
+// The rank is small, so a row's 2 * rank * len products cost little beside its
+// bytes: memory bounds all three kernels.  low and back are sums over a long
+// axis and the next product's input; they are kept as two 16-bit numbers (the
+// value's rounding and the rounding of what is left), 16 (bfloat16) or 22
+// (float16) bits of it, so that they cost no accuracy beside a 16-bit result
+// while both products run on the 16-bit matrix instructions.  float16's
+// exponents do not reach as far as 32-bit ones: a row of low is first scaled
+// by a power of two that puts its largest value just below the type's largest.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "launch.cuh"
+#include "lora.h"
+#include "ptx.cuh"
+
+namespace wqmm {
+namespace {
+
+constexpr int kThreads = 128;
+
+// ------------------------------------------------------------------ types
+template <bool BF16>
+struct Half;
+template <>
+struct Half<true> {
+  static __device__ __forceinline__ float get(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+  static __device__ __forceinline__ uint16_t put(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+  static __device__ __forceinline__ uint32_t put2(float a, float b) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+};
+template <>
+struct Half<false> {
+  static __device__ __forceinline__ float get(uint16_t v) { return __half2float(__ushort_as_half(v)); }
+  static __device__ __forceinline__ uint16_t put(float v) { return __half_as_ushort(__float2half_rn(v)); }
+  static __device__ __forceinline__ uint32_t put2(float a, float b) {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+};
+
+// d += a b: 16 x 8 x 16, 16-bit inputs, 32-bit sums.
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool has) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(has ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool has) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(has ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// ------------------------------------------------------------------ tiles of rows
+// Tile t of the sorted rows when every group of rows is cut into tiles of `bm`:
+// its group and its rows [p0, p1).  The groups are the adapters and, with
+// `bare`, the rows of none behind them.  The offsets are clamped to [0, m], so
+// that no value of theirs leads out of the tensors.  Called by whole warps.
+struct Tile {
+  int group;
+  int64_t p0, p1;
+};
+__device__ __forceinline__ int64_t offset_at(const LoraRows& r, int g) {
+  if (g > r.adapters) return r.m;
+  const int64_t v = r.offsets[g];
+  return v < 0 ? 0 : (v > r.m ? r.m : v);
+}
+__device__ __forceinline__ bool find_tile(const LoraRows& r, int bare, int bm, int64_t t, Tile& out) {
+  const int lane = threadIdx.x & 31;
+  const int groups = r.adapters + bare;
+  for (int g0 = 0; g0 < groups; g0 += 32) {
+    const int g = g0 + lane;
+    int64_t lo = 0, hi = 0;
+    if (g < groups) {
+      lo = offset_at(r, g);
+      hi = offset_at(r, g + 1);
+    }
+    const int64_t n = hi > lo ? (hi - lo + bm - 1) / bm : 0;
+    int64_t upto = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+    if (t < all) {
+      const int at = __popc(__ballot_sync(0xffffffffu, upto <= t));
+      const int64_t first = __shfl_sync(0xffffffffu, upto - n, at);
+      out.group = g0 + at;
+      out.p1 = __shfl_sync(0xffffffffu, hi, at);
+      out.p0 = __shfl_sync(0xffffffffu, lo, at) + (t - first) * bm;
+      if (out.p1 > out.p0 + bm) out.p1 = out.p0 + bm;
+      return true;
+    }
+    t -= all;
+  }
+  return false;
+}
+// Row of a sorted place, -1 behind the tile (or where the order names no row).
+__device__ __forceinline__ int64_t row_at(const LoraRows& r, int64_t p, int64_t p1) {
+  if (p >= p1) return -1;
+  const int64_t v = r.source[p];
+  return v >= 0 && v < r.m ? v : -1;
+}
+// Most tiles that m rows in `groups` groups can make.
+int64_t most_tiles(int64_t m, int groups, int bm) {
+  const int64_t g = std::min<int64_t>(groups, m);
+  return (m + g * (bm - 1)) / bm;
+}
+
+__host__ __device__ constexpr int padded_sixteenths(int rank) {
+  return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8;
+}
+
+// ------------------------------------------------------------------ launches
+// Calls f with the padded rank's sixteenth (1, 2, 4 or 8) as a constant.
+template <typename F>
+cudaError_t with_rank(int rank, F&& f) {
+  switch (padded_sixteenths(rank)) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 4: return f(std::integral_constant<int, 4>());
+    default: return f(std::integral_constant<int, 8>());
+  }
+}
+
+// Up to this many rows per group of rows a tile has 16 rows instead of 64.
+bool few_rows(const LoraRows& r) { return r.m <= 16 * static_cast<int64_t>(std::min<int64_t>(r.adapters, r.m)) || r.m <= 64; }
+
+}  // namespace
+}  // namespace wqmm

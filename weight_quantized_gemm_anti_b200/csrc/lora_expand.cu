@@ -1,0 +1,194 @@
+// lora_expand.cu -- the low-rank adapters' contraction over the rank, out = y + low W^T.
+#include "lora_common.cuh"
+
+namespace wqmm {
+namespace {
+
+// ------------------------------------------------------------------ expand
+// A CTA has BM rows and `chunks` times 128 columns.  A row's low values stay in
+// registers as the matrix instruction's first operand; the weights of 128
+// columns are staged in shared memory, the next ones while these are used.
+// The weights' columns are dealt to the instruction's tiles of eight such that
+// a thread's four results of a 32-column group are neighbours with the next
+// three tiles': column q * 8 + 2 j + e of the group is column 2 q + e of tile
+// j, so a thread adds and stores 16 bytes of a row at once, four threads 64.
+template <int RT, bool KM>
+struct ExpandSmem {
+  static constexpr int RP = RT * 16;
+  static constexpr int kPitch = KM ? RP * 2 + 16 : 256 + 16;
+  static constexpr int kBuf = (KM ? 128 : RP) * kPitch;
+  static constexpr int kBytes = 2 * kBuf;
+};
+
+template <bool BF16, int RT, bool KM, int WM>
+__global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandParams p, int rank, int chunks) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  constexpr int RP = RT * 16, BM = WM * 16;
+  constexpr int GROUPS = WM == 1 ? 1 : 4;  // 32-column groups of a chunk per warp
+  using L = ExpandSmem<RT, KM>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const uint32_t base = smem_u32(sm);
+  pdl_wait();
+  pdl_trigger();
+  Tile tile;
+  if (!find_tile(rows, p.bare, BM, blockIdx.x, tile)) return;
+  const bool with = tile.group < rows.adapters;
+  const uint16_t* w = p.w + static_cast<int64_t>(with ? tile.group : 0) * rank * p.len;
+  const int c_begin = blockIdx.y * chunks * 128;
+  const int c_end = min(c_begin + chunks * 128, p.len);
+
+  auto stage = [&](int c0, int buf) {
+    const uint32_t ws = base + buf * L::kBuf;
+    if constexpr (KM) {
+      constexpr int C = RP / 8;
+#pragma unroll
+      for (int i = 0; i < 128 * C / kThreads; ++i) {
+        const int at = tid + i * kThreads, col = at / C, c = at % C;
+        const bool has = c0 + col < c_end && c * 8 < rank;
+        // column (q, j, e) of its group of 32 goes to row (j, q, e)
+        const int in = col & 31, to = (col & ~31) | (((in >> 1) & 3) << 3) | ((in >> 3) << 1) | (in & 1);
+        cp16(ws + to * L::kPitch + c * 16, has ? w + static_cast<int64_t>(c0 + col) * rank + c * 8 : w, has);
+      }
+    } else {
+      // 64 bytes (32 columns) of one rank row per step: four chunks whose words change places
+#pragma unroll
+      for (int i = 0; i < (RP * 4 + kThreads - 1) / kThreads; ++i) {
+        const int at = tid + i * kThreads, r = at / 4, grp = at % 4;
+        if (r >= RP) break;
+        uint4 v[4];
+        const bool has = r < rank && c0 + grp * 32 < c_end;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[j] = has ? *reinterpret_cast<const uint4*>(w + static_cast<int64_t>(r) * p.len + c0 + grp * 32 + j * 8)
+                     : make_uint4(0, 0, 0, 0);
+        uint8_t* o = sm + buf * L::kBuf + r * L::kPitch + grp * 64;
+        *reinterpret_cast<uint4*>(o) = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+        *reinterpret_cast<uint4*>(o + 16) = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+        *reinterpret_cast<uint4*>(o + 32) = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+        *reinterpret_cast<uint4*>(o + 48) = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+      }
+    }
+    cp_async_commit();
+  };
+  if (with) stage(c_begin, 0);
+
+  // this thread's two rows: their places in y and out, and their low values
+  const int wrow = WM == 1 ? 0 : warp * 16;
+  int64_t row[2];
+  float factor[2] = {1.f, 1.f};
+  uint32_t a[2][RT][4];  // hi, lo
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t place = tile.p0 + wrow + g + 8 * i;
+    row[i] = row_at(rows, place, tile.p1);
+    const bool has = with && place < tile.p1;
+    if (!BF16 && has) factor[i] = p.low.factor[place];
+    const uint32_t* low = reinterpret_cast<const uint32_t*>(p.low.low + (has ? place * (2 * RP) : 0));
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int k = 0; k < RT; ++k) {
+        a[h][k][i] = has ? low[h * (RP / 2) + k * 8 + q] : 0u;
+        a[h][k][i + 2] = has ? low[h * (RP / 2) + k * 8 + 4 + q] : 0u;
+      }
+  }
+
+  int buf = 0;
+  for (int c0 = c_begin; c0 < c_end; c0 += 128, buf ^= 1) {
+    uint4 y[GROUPS][2];
+#pragma unroll
+    for (int s = 0; s < GROUPS; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = c0 + (WM == 1 ? warp : s) * 32 + q * 8;
+        y[s][i] = make_uint4(0, 0, 0, 0);
+        if (p.y.p && row[i] >= 0 && col < c_end)
+          y[s][i] = *reinterpret_cast<const uint4*>(p.y.p + row[i] * p.y.ld + col);
+      }
+    if (with) {
+      cp_async_wait_group<0>();
+      __syncthreads();
+      if (c0 + 128 < c_end) stage(c0 + 128, buf ^ 1);
+    }
+    const uint32_t ws = base + buf * L::kBuf;
+#pragma unroll
+    for (int s = 0; s < GROUPS; ++s) {
+      const int grp = WM == 1 ? warp : s;
+      float acc[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+      if (with) {
+#pragma unroll
+        for (int k = 0; k < RT; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            uint32_t b[4];
+            if constexpr (KM) {
+              const int r = grp * 32 + j * 8 + ((lane >> 4) << 3) + (lane & 7), c = k * 2 + ((lane >> 3) & 1);
+              ldsm4(b, ws + r * L::kPitch + c * 16);
+            } else {
+              const int r = k * 16 + (lane & 15), c = grp * 4 + j + (lane >> 4);
+              ldsm4t(b, ws + r * L::kPitch + c * 16);
+            }
+#pragma unroll
+            for (int h = 1; h >= 0; --h) {  // the small part first
+              mma<BF16>(acc[j], a[h][k], b[0], b[1]);
+              mma<BF16>(acc[j + 1], a[h][k], b[2], b[3]);
+            }
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = c0 + grp * 32 + q * 8;
+        if (row[i] < 0 || col >= c_end) continue;
+        const uint32_t yv[4] = {y[s][i].x, y[s][i].y, y[s][i].z, y[s][i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float v0 = acc[j][2 * i], v1 = acc[j][2 * i + 1];
+          const float y0 = Half<BF16>::get(yv[j] & 0xffff), y1 = Half<BF16>::get(yv[j] >> 16);
+          v0 = BF16 ? v0 + y0 : fmaf(factor[i], v0, y0);
+          v1 = BF16 ? v1 + y1 : fmaf(factor[i], v1, y1);
+          o[j] = with ? Half<BF16>::put2(v0, v1) : yv[j];
+        }
+        *reinterpret_cast<uint4*>(p.out + row[i] * p.ldo + col) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    // the buffer just read is filled again two chunks on, after the next barrier
+  }
+}
+
+template <bool BF16, int RT, bool KM, int WM>
+cudaError_t expand_as(const LoraRows& rows, const ExpandParams& p, int rank, int sms, cudaStream_t s) {
+  constexpr int BM = WM * 16;
+  const int64_t tiles = most_tiles(rows.m, rows.adapters + p.bare, BM);
+  // columns per CTA: up to 1024, fewer where there would be under eight CTAs per SM
+  const int all = (p.len + 127) / 128;
+  int chunks = 8;
+  while (chunks > 1 && tiles * ((all + chunks - 1) / chunks) < 8 * sms) chunks /= 2;
+  auto kernel = expand_kernel<BF16, RT, KM, WM>;
+  const size_t smem = ExpandSmem<RT, KM>::kBytes;
+  if (const cudaError_t e = allow_smem(kernel, smem); e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles), static_cast<unsigned>((all + chunks - 1) / chunks)),
+                    dim3(kThreads), smem, 1, s, rows, p, rank, chunks);
+}
+
+}  // namespace
+
+cudaError_t launch_lora_expand(const LoraRows& rows, const ExpandParams& p, int rank, bool rank_major, bool bf16,
+                               int sms, cudaStream_t s) {
+  return with_rank(rank, [&](auto rt) {
+    constexpr int RT = decltype(rt)::value;
+    auto pick = [&](auto t, auto km) {
+      return few_rows(rows) ? expand_as<decltype(t)::value, RT, decltype(km)::value, 1>(rows, p, rank, sms, s)
+                            : expand_as<decltype(t)::value, RT, decltype(km)::value, 4>(rows, p, rank, sms, s);
+    };
+    auto by_major = [&](auto t) { return rank_major ? pick(t, std::false_type()) : pick(t, std::true_type()); };
+    return bf16 ? by_major(std::true_type()) : by_major(std::false_type());
+  });
+}
+
+}  // namespace wqmm

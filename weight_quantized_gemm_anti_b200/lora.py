@@ -1,0 +1,86 @@
+"""Low-rank adapters of many requests beside a shared quantised projection, and their gradients.
+
+Every row of a batch has one adapter or none.  ``adapter_order`` sorts the rows
+by adapter once per batch; every projection of every layer then reads that
+order: ``lora_add`` adds the adapters' part to a projection's output (in place
+if asked), ``lora_weight_quant_matmul`` runs the quantised projection and that,
+and ``lora_grad`` gives the gradients for the input and the adapters (the
+projection's weight is frozen).
+
+Every call works on the tensors' device and on its current stream, or on
+``stream`` (a torch.cuda.Stream or a raw handle; the caller orders the inputs
+before it), and does not wait for the GPU.
+"""
+from __future__ import annotations
+
+from . import _both_phases, _desc_bytes, _placed, _same_device, lib, weight_quant_matmul
+from .routing import TokenOrder, sort_tokens
+
+
+def adapter_order(adapter_ids, num_adapters: int, stream=None) -> TokenOrder:
+    """The rows in the order of their adapters: adapter_ids (m), one index per row, int32 or int64; an index outside
+    [0, num_adapters) is a row without adapter.  For x1 of (b, s, k) the rows are counted through."""
+    return sort_tokens(adapter_ids.reshape(-1), num_adapters, stream)
+
+
+def lora_add(x1, lora_a, lora_b, order: TokenOrder, scale=None, y=None, out=None, stream=None):
+    """out[r] = y[r] + scale[a] * (x1[r] @ lora_a[a].T) @ lora_b[a].T, a the adapter of row r; a row without adapter
+    gets y, or zeros.  x1 (m, k) or (b, s, k); lora_a (adapters, rank, k); lora_b (adapters, n, rank); scale
+    (adapters) float32; ``out`` may be ``y``."""
+    import torch
+    device = _same_device(x1, lora_a, lora_b, order.offsets, order.source, scale, y, out)
+    where = _placed(device, stream)
+    if where is not None:
+        with where:
+            return lora_add(x1, lora_a, lora_b, order, scale, y, out)
+    if out is None:
+        out = torch.empty((*x1.shape[:-1], lora_b.shape[1]), dtype=x1.dtype, device=device)
+    L = lib()
+    _both_phases(L.lora_get_workspace_size, L.lora_run, device, _desc_bytes(x1), _desc_bytes(lora_a),
+                 _desc_bytes(lora_b), _desc_bytes(scale), _desc_bytes(order.offsets), _desc_bytes(order.source),
+                 _desc_bytes(y), _desc_bytes(out))
+    return out
+
+
+def lora_weight_quant_matmul(x1, x2_desc, antiquant_scale, lora_a, lora_b, order: TokenOrder, lora_scale=None,
+                             antiquant_offset=None, bias=None, x3=None, antiquant_group_size: int = 0, out=None,
+                             stream=None):
+    """The anti-quant projection of x1 with the rows' adapters added in place:
+    out = x1 @ ((x2 + antiquant_offset) * antiquant_scale) + bias + x3 + the adapters' part.  The projection is
+    rounded to the output type before the adapters' part is added, and the sum once more."""
+    device = _same_device(x1, antiquant_scale, antiquant_offset, bias, x3, out)
+    where = _placed(device, stream)
+    if where is not None:
+        with where:
+            return lora_weight_quant_matmul(x1, x2_desc, antiquant_scale, lora_a, lora_b, order, lora_scale,
+                                            antiquant_offset, bias, x3, antiquant_group_size, out)
+    out = weight_quant_matmul(x1, x2_desc, antiquant_scale, antiquant_offset, bias, x3, antiquant_group_size, out)
+    return lora_add(x1, lora_a, lora_b, order, lora_scale, y=out, out=out)
+
+
+def lora_grad(grad, x1, lora_a, lora_b, order: TokenOrder, scale=None, grad_x=None, need_grad_x: bool = True,
+              in_place: bool = False, stream=None):
+    """The gradients of ``lora_add`` given ``grad`` of its result (y's is ``grad`` itself): (for x1, lora_a, lora_b).
+    ``grad_x`` (m, k): what else x1's gradient has, the projection's own part, added in 32 bits before the one
+    rounding; with ``in_place`` the sum goes into that tensor.  ``need_grad_x`` False: None in x1's place."""
+    import torch
+    device = _same_device(grad, x1, lora_a, lora_b, order.offsets, order.source, scale, grad_x)
+    where = _placed(device, stream)
+    if where is not None:
+        with where:
+            return lora_grad(grad, x1, lora_a, lora_b, order, scale, grad_x, need_grad_x, in_place)
+    if grad_x is None and in_place:
+        raise ValueError("in_place needs a grad_x to add to")
+    if grad_x is not None and not need_grad_x:
+        raise ValueError("a grad_x is given, but need_grad_x is False")
+    out = None
+    if need_grad_x:
+        out = grad_x if in_place else torch.empty(x1.shape, dtype=x1.dtype, device=device)
+    grad_a = torch.empty(lora_a.shape, dtype=lora_a.dtype, device=device)
+    grad_b = torch.empty(lora_b.shape, dtype=lora_b.dtype, device=device)
+    L = lib()
+    _both_phases(L.lora_grad_get_workspace_size, L.lora_run, device, _desc_bytes(grad), _desc_bytes(x1),
+                 _desc_bytes(lora_a), _desc_bytes(lora_b), _desc_bytes(scale), _desc_bytes(order.offsets),
+                 _desc_bytes(order.source), _desc_bytes(grad_x), _desc_bytes(out), _desc_bytes(grad_a),
+                 _desc_bytes(grad_b))
+    return out, grad_a, grad_b
