@@ -390,21 +390,30 @@ def _placed(device: int, stream):
     return None if torch.cuda.current_device() == device else torch.cuda.device(device)
 
 
+def _raw_stream(device: int) -> int:
+    """Handle of the current stream of `device`, by the call that makes no stream object where torch has it."""
+    global _raw_stream
+    import torch
+    direct = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _raw_stream = direct or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
+
+
 def _both_phases(phase1, run, device: int, *args) -> None:
     """Phase 1 on descriptor bytes, the workspace, and phase 2 on the current stream of `device`."""
-    import torch
     ws, ex = ctypes.c_uint64(0), ctypes.c_void_p(None)
     st = phase1(*args, ctypes.byref(ws), ctypes.byref(ex))
     if st:
         check(st)
     size, space = ws.value, None
     if size:
+        import torch
         try:
             space = torch.empty(size, dtype=torch.uint8, device=device)
         except BaseException:
             wqmm_executor_destroy(ex)
             raise
-    st = run(space.data_ptr() if size else None, size, ex, torch.cuda.current_stream(device).cuda_stream)
+    st = run(space.data_ptr() if size else None, size, ex, _raw_stream(device))
     if st:
         check(st)
 

@@ -23,6 +23,8 @@ namespace {
 // slots 32 at a time, the lanes of one group ranked by lane.  Every count is a
 // whole number added in a fixed place, so the order is stable and the same in
 // every run.  Ids outside [0, groups) make one more group, behind the others.
+constexpr int kBatch = 4;
+
 template <typename IdT>
 __device__ __forceinline__ int group_of(const IdT* ids, int64_t i, int groups) {
   const IdT v = ids[i];
@@ -65,12 +67,26 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortParams p) {
   const int run = ((p.chunk + warps - 1) / warps + 31) & ~31;
   const int64_t r0 = min(lo + static_cast<int64_t>(warp) * run, hi), r1 = min(r0 + run, hi);
   int* mine = next + warp * buckets;
-  for (int64_t i0 = r0; i0 < r1; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const int e = i < r1 ? group_of(ids, i, p.groups) : -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
+  // The ids of a batch are loaded together, so that their latency is paid once;
+  // a run of one batch keeps its groups for the second walk.
+  int group[kBatch];
+  auto load = [&](int64_t i0) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int64_t i = i0 + b * 32 + lane;
+      group[b] = i < r1 ? group_of(ids, i, p.groups) : -1;
+    }
+  };
+  for (int64_t i0 = r0; i0 < r1; i0 += 32 * kBatch) {
+    load(i0);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (i0 + b * 32 < r1) {
+        const uint32_t same = __match_any_sync(0xffffffffu, group[b]);
+        if (group[b] >= 0 && lane == __ffs(same) - 1) mine[group[b]] += __popc(same);
+        __syncwarp();
+      }
+    }
   }
   __syncthreads();
 
@@ -127,18 +143,24 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortParams p) {
   }
   __syncthreads();
 
-  for (int64_t i0 = r0; i0 < r1; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const int e = i < r1 ? group_of(ids, i, p.groups) : -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0) {
-      const int place = total[e] + mine[e] + __popc(same & ((1u << lane) - 1));
-      p.source[place] = static_cast<int>(i);
-      p.position[i] = e < p.groups ? place : -1;
+  for (int64_t i0 = r0; i0 < r1; i0 += 32 * kBatch) {
+    if (r1 - r0 > 32 * kBatch) load(i0);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int64_t i = i0 + b * 32 + lane;
+      if (i0 + b * 32 < r1) {
+        const int e = group[b];
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0) {
+          const int place = total[e] + mine[e] + __popc(same & ((1u << lane) - 1));
+          p.source[place] = static_cast<int>(i);
+          p.position[i] = e < p.groups ? place : -1;
+        }
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+      }
     }
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
   }
 }
 
@@ -288,11 +310,11 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineParams p, int tpt) 
 // grad_sorted[pos] = w * grad, and the dot product of grad with the row.  The
 // dot products are summed per thread, over the warp by shuffles and over the
 // token's warps in shared memory, always in the same order.
-template <int TYPE, int N>
+// B: slots of one pass over the gradient.
+template <int TYPE, int N, int B>
 __global__ void __launch_bounds__(256) combine_grad_kernel(CombineGradParams p, int tpt) {
   using E = Elem<TYPE>;
   using P = Pack<TYPE, N>;
-  constexpr int B = 8;  // slots of one pass over the gradient
   __shared__ float part[8][B];
   pdl_wait();
   pdl_trigger();
@@ -386,12 +408,19 @@ cudaError_t combine_as(const CombineParams& p, cudaStream_t s) {
   return launch_pdl(combine_kernel<TYPE, N>, grid, dim3(256), 0, 1, s, p, tpt);
 }
 
-template <int TYPE, int N>
-cudaError_t combine_grad_as(const CombineGradParams& p, cudaStream_t s) {
+template <int TYPE, int N, int B>
+cudaError_t combine_grad_slots(const CombineGradParams& p, cudaStream_t s) {
   const int tpt = threads_per_row(p.hidden / N, 32);
   const int per = 256 / tpt;
-  return launch_pdl(combine_grad_kernel<TYPE, N>, dim3(static_cast<unsigned>((p.tokens + per - 1) / per)), dim3(256),
-                    0, 1, s, p, tpt);
+  return launch_pdl(combine_grad_kernel<TYPE, N, B>, dim3(static_cast<unsigned>((p.tokens + per - 1) / per)),
+                    dim3(256), 0, 1, s, p, tpt);
+}
+
+template <int TYPE, int N>
+cudaError_t combine_grad_as(const CombineGradParams& p, cudaStream_t s) {
+  return p.top <= 2   ? combine_grad_slots<TYPE, N, 2>(p, s)
+         : p.top <= 4 ? combine_grad_slots<TYPE, N, 4>(p, s)
+                      : combine_grad_slots<TYPE, N, 8>(p, s);
 }
 
 template <int TYPE>

@@ -29,18 +29,25 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
   const uint32_t base = smem_u32(sm);
-  pdl_wait();
-  pdl_trigger();
   Tile tile;
-  if (!find_tile(rows, p.bare, BM, blockIdx.x, tile)) return;
+  // The launch before this one has waited for all that came before it, and what it
+  // writes itself is low: the order, the weights and y are read while it ends.
+  if (!find_tile(rows, p.bare, BM, blockIdx.x, tile)) {
+    pdl_wait();
+    return;
+  }
   const bool with = tile.group < rows.adapters;
   const uint16_t* w = p.w + static_cast<int64_t>(with ? tile.group : 0) * rank * p.len;
   const int c_begin = blockIdx.y * chunks * 128;
   const int c_end = min(c_begin + chunks * 128, p.len);
 
-  auto stage = [&](int c0, int buf) {
-    const uint32_t ws = base + buf * L::kBuf;
+  constexpr int WR = KM ? 1 : (RP * 4 + kThreads - 1) / kThreads;
+  uint4 wr[WR][4];
+  // k-major: copies under way in shared memory; rank-major: 64 bytes (32 columns) of a rank row per
+  // thread and step, in registers until put() changes their words' places
+  auto fetch = [&](int c0, int buf) {
     if constexpr (KM) {
+      const uint32_t ws = base + buf * L::kBuf;
       constexpr int C = RP / 8;
 #pragma unroll
       for (int i = 0; i < 128 * C / kThreads; ++i) {
@@ -50,38 +57,64 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
         const int in = col & 31, to = (col & ~31) | (((in >> 1) & 3) << 3) | ((in >> 3) << 1) | (in & 1);
         cp16(ws + to * L::kPitch + c * 16, has ? w + static_cast<int64_t>(c0 + col) * rank + c * 8 : w, has);
       }
+      cp_async_commit();
     } else {
-      // 64 bytes (32 columns) of one rank row per step: four chunks whose words change places
 #pragma unroll
-      for (int i = 0; i < (RP * 4 + kThreads - 1) / kThreads; ++i) {
-        const int at = tid + i * kThreads, r = at / 4, grp = at % 4;
-        if (r >= RP) break;
-        uint4 v[4];
-        const bool has = r < rank && c0 + grp * 32 < c_end;
+      for (int i = 0; i < WR; ++i) {
+        const int at = tid + i * kThreads, r = at / 4, col = c0 + (at % 4) * 32;
+        const bool has = r < rank && col < c_end;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          v[j] = has ? *reinterpret_cast<const uint4*>(w + static_cast<int64_t>(r) * p.len + c0 + grp * 32 + j * 8)
-                     : make_uint4(0, 0, 0, 0);
-        uint8_t* o = sm + buf * L::kBuf + r * L::kPitch + grp * 64;
+          wr[i][j] = has ? *reinterpret_cast<const uint4*>(w + static_cast<int64_t>(r) * p.len + col + j * 8)
+                         : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  auto put = [&](int buf) {
+    if constexpr (KM) {
+      cp_async_wait_group<0>();
+    } else {
+#pragma unroll
+      for (int i = 0; i < WR; ++i) {
+        const int at = tid + i * kThreads, r = at / 4;
+        if (r >= RP) break;
+        const uint4* v = wr[i];
+        uint8_t* o = sm + buf * L::kBuf + r * L::kPitch + (at % 4) * 64;
         *reinterpret_cast<uint4*>(o) = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
         *reinterpret_cast<uint4*>(o + 16) = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
         *reinterpret_cast<uint4*>(o + 32) = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
         *reinterpret_cast<uint4*>(o + 48) = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
       }
     }
-    cp_async_commit();
   };
-  if (with) stage(c_begin, 0);
+  if (with) fetch(c_begin, 0);
 
-  // this thread's two rows: their places in y and out, and their low values
+  // this thread's two rows: their places in y and out
   const int wrow = WM == 1 ? 0 : warp * 16;
   int64_t row[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) row[i] = row_at(rows, tile.p0 + wrow + g + 8 * i, tile.p1);
+  uint4 y[GROUPS][2];
+  auto fetch_y = [&](int c0) {
+#pragma unroll
+    for (int s = 0; s < GROUPS; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = c0 + (WM == 1 ? warp : s) * 32 + q * 8;
+        y[s][i] = make_uint4(0, 0, 0, 0);
+        if (p.y.p && row[i] >= 0 && col < c_end)
+          y[s][i] = *reinterpret_cast<const uint4*>(p.y.p + row[i] * p.y.ld + col);
+      }
+  };
+  fetch_y(c_begin);
+  pdl_wait();
+  pdl_trigger();
+
   float factor[2] = {1.f, 1.f};
   uint32_t a[2][RT][4];  // hi, lo
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int64_t place = tile.p0 + wrow + g + 8 * i;
-    row[i] = row_at(rows, place, tile.p1);
     const bool has = with && place < tile.p1;
     if (!BF16 && has) factor[i] = p.low.factor[place];
     const uint32_t* low = reinterpret_cast<const uint32_t*>(p.low.low + (has ? place * (2 * RP) : 0));
@@ -96,20 +129,11 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
 
   int buf = 0;
   for (int c0 = c_begin; c0 < c_end; c0 += 128, buf ^= 1) {
-    uint4 y[GROUPS][2];
-#pragma unroll
-    for (int s = 0; s < GROUPS; ++s)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int col = c0 + (WM == 1 ? warp : s) * 32 + q * 8;
-        y[s][i] = make_uint4(0, 0, 0, 0);
-        if (p.y.p && row[i] >= 0 && col < c_end)
-          y[s][i] = *reinterpret_cast<const uint4*>(p.y.p + row[i] * p.y.ld + col);
-      }
+    if (c0 > c_begin) fetch_y(c0);
     if (with) {
-      cp_async_wait_group<0>();
-      __syncthreads();
-      if (c0 + 128 < c_end) stage(c0 + 128, buf ^ 1);
+      put(buf);
+      __syncthreads();  // this chunk's weights are there, and the other buffer is read no more
+      if (c0 + 128 < c_end) fetch(c0 + 128, buf ^ 1);
     }
     const uint32_t ws = base + buf * L::kBuf;
 #pragma unroll
@@ -157,7 +181,6 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
         *reinterpret_cast<uint4*>(p.out + row[i] * p.ldo + col) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-    // the buffer just read is filled again two chunks on, after the next barrier
   }
 }
 

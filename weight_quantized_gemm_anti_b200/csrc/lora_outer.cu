@@ -36,11 +36,58 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(LoraRows rows, OuterPar
   const OuterParams& p = ct < tiles0 ? p0 : p1;
   const int c0 = (ct < tiles0 ? ct : ct - tiles0) * 128;
   const int adapter = blockIdx.y;
-  pdl_wait();
-  pdl_trigger();
   const int64_t lo = offset_at(rows, adapter), hi = max(offset_at(rows, adapter + 1), lo);
   const int64_t steps = (hi - lo + 63) / 64;
   const int64_t s0 = steps * crank / cs, s1 = steps * (crank + 1) / cs;
+
+  // this thread's rows of x in a step: 16-byte chunk tid % 16 of rows tid / 16 + 8 i.  Their numbers are
+  // loaded a step before the rows are.
+  const int xc = tid & 15;
+  const bool in = c0 + xc * 8 < p.len;
+  int64_t next[8];
+  auto find = [&](int64_t step) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) next[i] = step < s1 ? row_at(rows, lo + step * 64 + tid / 16 + 8 * i, hi) : -1;
+  };
+  auto load_x = [&](int stage) {
+    const uint32_t xs = base + stage * L::kStage;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = tid / 16 + 8 * i;
+      const bool has = in && next[i] >= 0;
+      cp16(xs + r * L::kXPitch + xc * 16, has ? p.x.p + next[i] * p.x.ld + c0 + xc * 8 : p.x.p, has);
+    }
+  };
+  auto load_low = [&](int64_t step, int stage) {
+    const uint32_t ls = base + stage * L::kStage + L::kX, fs = ls + L::kL;
+    const int64_t r0 = lo + step * 64;
+    constexpr int C = RP / 4;  // 16-byte chunks of a row of low
+#pragma unroll
+    for (int i = 0; i < 64 * C / kThreads; ++i) {
+      const int at = tid + i * kThreads, r = at / C, cc = at % C;
+      const bool has = r0 + r < hi;
+      cp16(ls + r * L::kLPitch + cc * 16, has ? p.low.low + (r0 + r) * (2 * RP) + cc * 8 : p.low.low, has);
+    }
+    if (!BF16 && tid < 64) {
+      const bool has = r0 + tid < hi;
+      cp4(fs + tid * 4, has ? p.low.factor + r0 + tid : p.low.factor, has);
+    }
+  };
+  // x and the order are older than the launch before this one, which has waited for all that
+  // came before it: they are read while it ends, low after that
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) {
+    find(s0 + i);
+    if (s0 + i < s1) load_x(i);
+  }
+  find(s0 + S - 1);
+  pdl_wait();
+  pdl_trigger();
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) {
+    if (s0 + i < s1) load_low(s0 + i, i);
+    cp_async_commit();
+  }
 
   // the largest factor of this CTA's rows: the others' low values are scaled to it
   float top = 1.f, below = 1.f;
@@ -56,31 +103,6 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(LoraRows rows, OuterPar
     below = 1.f / top;            // of a power of two: exact
   }
 
-  auto load = [&](int64_t step, int stage) {
-    const uint32_t xs = base + stage * L::kStage, ls = xs + L::kX, fs = ls + L::kL;
-    const int64_t r0 = lo + step * 64;
-    const int c = tid & 15;
-    const bool in = c0 + c * 8 < p.len;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = tid / 16 + 8 * i;
-      const int64_t row = row_at(rows, r0 + r, hi);
-      const bool has = in && row >= 0;
-      cp16(xs + r * L::kXPitch + c * 16, has ? p.x.p + row * p.x.ld + c0 + c * 8 : p.x.p, has);
-    }
-    constexpr int C = RP / 4;  // 16-byte chunks of a row of low
-#pragma unroll
-    for (int i = 0; i < 64 * C / kThreads; ++i) {
-      const int at = tid + i * kThreads, r = at / C, cc = at % C;
-      const bool has = r0 + r < hi;
-      cp16(ls + r * L::kLPitch + cc * 16, has ? p.low.low + (r0 + r) * (2 * RP) + cc * 8 : p.low.low, has);
-    }
-    if (!BF16 && tid < 64) {
-      const bool has = r0 + tid < hi;
-      cp4(fs + tid * 4, has ? p.low.factor + r0 + tid : p.low.factor, has);
-    }
-  };
-
   float acc[2][NT][4];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -89,16 +111,16 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(LoraRows rows, OuterPar
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
 
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) {
-    if (s0 + i < s1) load(s0 + i, i);
-    cp_async_commit();
-  }
   for (int64_t st = s0; st < s1; ++st) {
     cp_async_wait_group<S - 2>();
     __syncthreads();
-    if (st + S - 1 < s1) load(st + S - 1, static_cast<int>((st - s0 + S - 1) % S));
+    if (st + S - 1 < s1) {
+      const int stage = static_cast<int>((st - s0 + S - 1) % S);
+      load_x(stage);
+      load_low(st + S - 1, stage);
+    }
     cp_async_commit();
+    find(st + S);
     const uint32_t xs = base + static_cast<int>((st - s0) % S) * L::kStage, ls = xs + L::kX;
     const float* fs = reinterpret_cast<const float*>(sm + static_cast<int>((st - s0) % S) * L::kStage + L::kX + L::kL);
 #pragma unroll
@@ -172,13 +194,20 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(LoraRows rows, OuterPar
       r[1] = r[0] + 1;
     }
     if (c0 + c[0] >= p.len) continue;
-    float v[2] = {0.f, 0.f};
-    for (int k = 0; k < cs; ++k)
+    float f[8][2], v[2] = {0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t a = smem_u32(red + c[i] * L::kRedPitch + r[i]);
-        v[i] += ld_cluster_f32(cs > 1 ? mapa_shared(a, k) : a);
-      }
+    for (int k = 0; k < 8; ++k)
+      if (k < cs)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t a = smem_u32(red + c[i] * L::kRedPitch + r[i]);
+          f[k][i] = ld_cluster_f32(cs > 1 ? mapa_shared(a, k) : a);
+        }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < cs)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[i] += f[k][i];
     const int64_t to = p.rank_rows ? static_cast<int64_t>(r[0]) * p.len + c0 + c[0]
                                    : static_cast<int64_t>(c0 + c[0]) * rank + r[0];
     *reinterpret_cast<uint32_t*>(out + to) = Half<BF16>::put2(v[0], v[1]);

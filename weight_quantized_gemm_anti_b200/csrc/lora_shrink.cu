@@ -20,6 +20,52 @@ struct ShrinkSmem {
   static constexpr int kBytes = kStage * kStages;
 };
 
+// Few rows, k-major weights: nothing is shared between the warps, so the
+// matrix instruction's operands come straight from global memory.  A thread
+// loads 16 bytes of its rows and of its weight rows, eight neighbours of the
+// contraction; four threads' 32 make two steps of the instruction.  Which
+// element stands for which of a step's sixteen does not matter to the sum as
+// long as both operands agree.  Each warp takes every fourth 32.
+template <bool BF16, int RT>
+__device__ __forceinline__ void few_rows_sum(const LoraRows& rows, const ShrinkParams& p, int rank, const Tile& tile,
+                                             int k0, int k1, float (&acc)[RT * 2][4]) {
+  constexpr int NT = RT * 2;
+  constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;  // 32s in flight: 16 to 18 loads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const uint16_t* x[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t r = row_at(rows, tile.p0 + g + 8 * i, tile.p1);
+    x[i] = r >= 0 ? p.x.p + r * p.x.ld + q * 8 : nullptr;
+  }
+  const uint16_t* w = p.w + (static_cast<int64_t>(tile.group) * rank + g) * p.len + q * 8;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int k = k0 + warp * 32; k < k1; k += 128 * U) {
+    uint4 xv[U][2], wv[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = k + u * 128;
+      const bool in = at < k1;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        wv[u][n] = in && n * 8 < rank
+                       ? *reinterpret_cast<const uint4*>(w + static_cast<int64_t>(n) * 8 * p.len + at) : zero;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) xv[u][i] = in && x[i] ? *reinterpret_cast<const uint4*>(x[i] + at) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t a0[4] = {xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y};
+      const uint32_t a1[4] = {xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma<BF16>(acc[n], a0, wv[u][n].x, wv[u][n].y);
+        mma<BF16>(acc[n], a1, wv[u][n].z, wv[u][n].w);
+      }
+    }
+  }
+}
+
 template <bool BF16, int RT, bool KM, int WM>
 __device__ __forceinline__ void shrink_tile(const LoraRows& rows, const ShrinkParams& p, int rank, int cs,
                                             const Tile& tile, uint8_t* sm) {
@@ -32,6 +78,15 @@ __device__ __forceinline__ void shrink_tile(const LoraRows& rows, const ShrinkPa
   const int steps_all = (p.len + 63) / 64;
   const int s0 = static_cast<int>(static_cast<int64_t>(steps_all) * crank / cs);
   const int s1 = static_cast<int>(static_cast<int64_t>(steps_all) * (crank + 1) / cs);
+  float acc[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+  const int wrow = WM == 1 ? 0 : warp * 16;
+  if constexpr (WM == 1 && KM) {
+    few_rows_sum<BF16, RT>(rows, p, rank, tile, s0 * 64, min(s1 * 64, p.len), acc);
+  } else {
   const uint16_t* w = p.w + static_cast<int64_t>(tile.group) * rank * p.len;
 
   // this thread's rows of x: 16-byte chunk tid % 8 of rows tid / 8 + 16 i
@@ -72,18 +127,11 @@ __device__ __forceinline__ void shrink_tile(const LoraRows& rows, const ShrinkPa
     }
   };
 
-  float acc[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) {
     if (s0 + i < s1) load(s0 + i, i);
     cp_async_commit();
   }
-  const int wrow = WM == 1 ? 0 : warp * 16;
   for (int st = s0; st < s1; ++st) {
     cp_async_wait_group<S - 2>();
     __syncthreads();
@@ -116,16 +164,23 @@ __device__ __forceinline__ void shrink_tile(const LoraRows& rows, const ShrinkPa
   cp_async_wait_group<0>();
   __syncthreads();
 
-  // sums to shared memory: [WM == 1: warp][row][RP]
+  }
+
+  // sums to shared memory, [row][RP]; with WM == 1 the warps' behind it first
   float* red = reinterpret_cast<float*>(sm);
   {
-    float* mine = red + (WM == 1 ? warp * 16 * RP : wrow * RP);
+    float* mine = red + (WM == 1 ? (1 + warp) * 16 * RP : wrow * RP);
     const int g = lane >> 2, q = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       *reinterpret_cast<float2*>(mine + g * RP + n * 8 + 2 * q) = make_float2(acc[n][0], acc[n][1]);
       *reinterpret_cast<float2*>(mine + (g + 8) * RP + n * 8 + 2 * q) = make_float2(acc[n][2], acc[n][3]);
     }
+  }
+  if constexpr (WM == 1) {
+    __syncthreads();
+    for (int at = tid; at < 16 * RP; at += kThreads)
+      red[at] = (red[16 * RP + at] + red[32 * RP + at]) + (red[48 * RP + at] + red[64 * RP + at]);
   }
   if (cs > 1)
     cluster_sync();
@@ -134,7 +189,6 @@ __device__ __forceinline__ void shrink_tile(const LoraRows& rows, const ShrinkPa
 
   // four values of a row per lane; the CTAs of the cluster share the rows
   constexpr int LANES = RP / 4, PER = kThreads / LANES;
-  constexpr int PARTS = WM == 1 ? 4 : 1;
   const int sub = tid % LANES;
   const float scale = p.scale ? p.scale[tile.group] : 1.f;
   for (int r0 = crank * PER; r0 < BM; r0 += cs * PER) {
@@ -143,15 +197,18 @@ __device__ __forceinline__ void shrink_tile(const LoraRows& rows, const ShrinkPa
     const bool live = r < BM && place < tile.p1;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (live) {
-      for (int c = 0; c < cs; ++c)
+      const uint32_t at = smem_u32(red + r * RP + sub * 4);
+      float4 f[8];  // all CTAs' parts in flight at once
 #pragma unroll
-        for (int w0 = 0; w0 < PARTS; ++w0) {
-          const uint32_t at = smem_u32(red + (w0 * 16 + r) * RP + sub * 4);
-          const float4 f = ld_cluster_f32x4(cs > 1 ? mapa_shared(at, c) : at);
-          v[0] += f.x;
-          v[1] += f.y;
-          v[2] += f.z;
-          v[3] += f.w;
+      for (int c = 0; c < 8; ++c)
+        if (c < cs) f[c] = ld_cluster_f32x4(cs > 1 ? mapa_shared(at, c) : at);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < cs) {
+          v[0] += f[c].x;
+          v[1] += f[c].y;
+          v[2] += f[c].z;
+          v[3] += f[c].w;
         }
     }
 #pragma unroll
@@ -218,9 +275,9 @@ cudaError_t shrink_as(const LoraRows& rows, const ShrinkParams* p, int rank, int
   // shares of the contraction: as many as fill the SMs four times over, each of at least four steps of 64
   int cs = 1;
   while (cs < 8 && tiles * (BOTH ? 2 : 1) * cs < 4 * sms && (len + 63) / 64 >= 8 * cs) cs *= 2;
-  size_t smem = ShrinkSmem<RT, true, BM>::kBytes;
+  size_t smem = WM == 1 ? 0 : ShrinkSmem<RT, true, BM>::kBytes;
   if (BOTH) smem = std::max<size_t>(smem, ShrinkSmem<RT, false, BM>::kBytes);
-  smem = std::max<size_t>(smem, static_cast<size_t>(WM == 1 ? 64 : BM) * RT * 16 * 4);
+  smem = std::max<size_t>(smem, static_cast<size_t>(WM == 1 ? 80 : BM) * RT * 16 * 4);
   auto kernel = shrink_kernel<BF16, RT, WM, BOTH>;
   if (const cudaError_t e = allow_smem(kernel, smem); e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs), BOTH ? 2 : 1), dim3(kThreads), smem, cs, s, rows,

@@ -13,6 +13,8 @@ before it), and does not wait for the GPU.
 """
 from __future__ import annotations
 
+import torch
+
 from . import _both_phases, _desc_bytes, _placed, _same_device, lib, weight_quant_matmul
 from .routing import TokenOrder, sort_tokens
 
@@ -27,14 +29,13 @@ def lora_add(x1, lora_a, lora_b, order: TokenOrder, scale=None, y=None, out=None
     """out[r] = y[r] + scale[a] * (x1[r] @ lora_a[a].T) @ lora_b[a].T, a the adapter of row r; a row without adapter
     gets y, or zeros.  x1 (m, k) or (b, s, k); lora_a (adapters, rank, k); lora_b (adapters, n, rank); scale
     (adapters) float32; ``out`` may be ``y``."""
-    import torch
     device = _same_device(x1, lora_a, lora_b, order.offsets, order.source, scale, y, out)
     where = _placed(device, stream)
     if where is not None:
         with where:
             return lora_add(x1, lora_a, lora_b, order, scale, y, out)
     if out is None:
-        out = torch.empty((*x1.shape[:-1], lora_b.shape[1]), dtype=x1.dtype, device=device)
+        out = x1.new_empty((*x1.shape[:-1], lora_b.shape[1]))
     L = lib()
     _both_phases(L.lora_get_workspace_size, L.lora_run, device, _desc_bytes(x1), _desc_bytes(lora_a),
                  _desc_bytes(lora_b), _desc_bytes(scale), _desc_bytes(order.offsets), _desc_bytes(order.source),
@@ -63,7 +64,6 @@ def lora_grad(grad, x1, lora_a, lora_b, order: TokenOrder, scale=None, grad_x=No
     """The gradients of ``lora_add`` given ``grad`` of its result (y's is ``grad`` itself): (for x1, lora_a, lora_b).
     ``grad_x`` (m, k): what else x1's gradient has, the projection's own part, added in 32 bits before the one
     rounding; with ``in_place`` the sum goes into that tensor.  ``need_grad_x`` False: None in x1's place."""
-    import torch
     device = _same_device(grad, x1, lora_a, lora_b, order.offsets, order.source, scale, grad_x)
     where = _placed(device, stream)
     if where is not None:
@@ -75,9 +75,9 @@ def lora_grad(grad, x1, lora_a, lora_b, order: TokenOrder, scale=None, grad_x=No
         raise ValueError("a grad_x is given, but need_grad_x is False")
     out = None
     if need_grad_x:
-        out = grad_x if in_place else torch.empty(x1.shape, dtype=x1.dtype, device=device)
-    grad_a = torch.empty(lora_a.shape, dtype=lora_a.dtype, device=device)
-    grad_b = torch.empty(lora_b.shape, dtype=lora_b.dtype, device=device)
+        out = grad_x if in_place else x1.new_empty(x1.shape)
+    grad_a = lora_a.new_empty(lora_a.shape)
+    grad_b = lora_b.new_empty(lora_b.shape)
     L = lib()
     _both_phases(L.lora_grad_get_workspace_size, L.lora_run, device, _desc_bytes(grad), _desc_bytes(x1),
                  _desc_bytes(lora_a), _desc_bytes(lora_b), _desc_bytes(scale), _desc_bytes(order.offsets),

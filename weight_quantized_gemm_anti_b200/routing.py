@@ -18,6 +18,8 @@ from __future__ import annotations
 
 from typing import NamedTuple, Optional, Sequence
 
+import torch
+
 from . import _both_phases, _desc_bytes, _placed, _same_device, lib, weight_quant_matmul
 
 
@@ -31,7 +33,6 @@ class TokenOrder(NamedTuple):
 def sort_tokens(expert_ids, num_experts: int, stream=None) -> TokenOrder:
     """The stable order of the slots by expert: expert_ids (T), (T, K) or (b, s, K), int32 or int64; an id outside
     [0, num_experts) belongs to no expert (a dropped slot, or an expert of another rank)."""
-    import torch
     device = _same_device(expert_ids)
     where = _placed(device, stream)
     if where is not None:
@@ -39,9 +40,9 @@ def sort_tokens(expert_ids, num_experts: int, stream=None) -> TokenOrder:
             return sort_tokens(expert_ids, num_experts)
     if not expert_ids.is_contiguous():
         raise ValueError("expert_ids must be contiguous")
-    offsets = torch.empty(max(int(num_experts), 0) + 1, dtype=torch.int32, device=device)
-    source = torch.empty(expert_ids.numel(), dtype=torch.int32, device=device)
-    position = torch.empty(expert_ids.shape, dtype=torch.int32, device=device)
+    offsets = expert_ids.new_empty(max(int(num_experts), 0) + 1, dtype=torch.int32)
+    source = expert_ids.new_empty(expert_ids.numel(), dtype=torch.int32)
+    position = torch.empty_like(expert_ids, dtype=torch.int32)
     L = lib()
     _both_phases(L.route_sort_get_workspace_size, L.route_run, device, _desc_bytes(expert_ids), int(num_experts),
                  _desc_bytes(offsets), _desc_bytes(source), _desc_bytes(position))
@@ -52,14 +53,13 @@ def dispatch_tokens(x, order: TokenOrder, out=None, stream=None):
     """out[position[t, j]] = x[t] for every slot of an expert; x (T, hidden) or (b, s, hidden).  ``out``: (rows,
     hidden) of x's dtype, one row per slot unless given; rows of no slot keep what they hold (in an ``out`` made
     here that is uninitialised memory, behind order.offsets[-1])."""
-    import torch
     device = _same_device(x, order.position, out)
     where = _placed(device, stream)
     if where is not None:
         with where:
             return dispatch_tokens(x, order, out)
     if out is None:
-        out = torch.empty((order.position.numel(), x.shape[-1]), dtype=x.dtype, device=device)
+        out = x.new_empty((order.position.numel(), x.shape[-1]))
     L = lib()
     _both_phases(L.route_dispatch_get_workspace_size, L.route_run, device, _desc_bytes(x),
                  _desc_bytes(order.position), _desc_bytes(out))
@@ -70,16 +70,18 @@ def combine_tokens(x_sorted, order: TokenOrder, weights=None, x3=None, out=None,
     """out[t] = x3[t] + sum_j weights[t, j] * x_sorted[position[t, j]], in 32 bits, rounded once.  ``weights``:
     shape of position, float16, bfloat16 or float32; None: all one, which is also the gradient of
     ``dispatch_tokens``.  ``out``: (T, hidden) unless x3 or ``out`` says (b, s, hidden)."""
-    import torch
     device = _same_device(x_sorted, order.position, weights, x3, out)
     where = _placed(device, stream)
     if where is not None:
         with where:
             return combine_tokens(x_sorted, order, weights, x3, out)
     if out is None:
-        p = order.position
-        shape = x3.shape if x3 is not None else (p.shape if p.dim() == 1 else p.shape[:-1]) + x_sorted.shape[-1:]
-        out = torch.empty(shape, dtype=x_sorted.dtype, device=device)
+        if x3 is not None:
+            out = torch.empty_like(x3)
+        else:
+            p = order.position.shape
+            tokens = p if len(p) == 1 else p[:-1]
+            out = x_sorted.new_empty((*tokens, x_sorted.shape[-1]))
     L = lib()
     _both_phases(L.route_combine_get_workspace_size, L.route_run, device, _desc_bytes(x_sorted),
                  _desc_bytes(order.position), _desc_bytes(weights), _desc_bytes(x3), _desc_bytes(out))
@@ -90,7 +92,6 @@ def combine_tokens_grad(grad, x_sorted, order: TokenOrder, weights, out=None, st
     """The gradient of ``combine_tokens`` for x_sorted and weights, given ``grad`` of its result:
     (grad_sorted, grad_weights).  Rows of no slot keep what ``out`` (grad_sorted's tensor, made here unless given)
     holds; grad_weights of a slot of no expert is 0."""
-    import torch
     device = _same_device(grad, x_sorted, order.position, weights, out)
     where = _placed(device, stream)
     if where is not None:
@@ -113,7 +114,6 @@ def expert_weight_quant_matmul(x_sorted, order: TokenOrder, x2_descs: Sequence, 
     """out[rows of e] = the anti-quant GEMM of expert e's rows of x_sorted with its weight, for every expert that
     has rows.  ``bounds``: order.offsets on the host (None: read here, which waits for the stream).  Rows behind
     the last expert keep what ``out`` holds."""
-    import torch
     device = _same_device(x_sorted, out)
     where = _placed(device, stream)
     if where is not None:
@@ -125,7 +125,7 @@ def expert_weight_quant_matmul(x_sorted, order: TokenOrder, x2_descs: Sequence, 
     if len(bounds) != len(x2_descs) + 1:
         raise ValueError(f"{len(x2_descs)} weights for {len(bounds) - 1} experts")
     if out is None:
-        out = torch.empty((x_sorted.shape[0], x2_descs[0].shape[1]), dtype=x_sorted.dtype, device=device)
+        out = x_sorted.new_empty((x_sorted.shape[0], x2_descs[0].shape[1]))
     for e, desc in enumerate(x2_descs):
         lo, hi = bounds[e], bounds[e + 1]
         if lo < hi:
