@@ -6,6 +6,9 @@
 
 #include <cstdint>
 
+#include "host.h"
+#include "internal.h"
+
 namespace wqmm {
 
 // The rows in the order of their adapters.
@@ -58,11 +61,12 @@ struct OuterParams {
 };
 
 int lora_padded_rank(int rank);
-cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
+// x by x k-major weights, and with count 2 then by rank-major ones.
+wqmm_status launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
                                cudaStream_t s);
 cudaError_t launch_lora_expand(const LoraRows& rows, const ExpandParams& p, int rank, bool rank_major, bool bf16,
                                int sms, cudaStream_t s);
-cudaError_t launch_lora_outer(const LoraRows& rows, const OuterParams (&p)[2], int rank, bool bf16, int sms,
+wqmm_status launch_lora_outer(const LoraRows& rows, const OuterParams (&p)[2], int rank, bool bf16, int sms,
                               cudaStream_t s);
 
 }  // namespace wqmm

@@ -1,194 +1,20 @@
 // lora_shrink.cu -- the low-rank adapters' contractions over a long axis, low = scale * x W^T.
-#include "lora_common.cuh"
+#include "lora_tc.cuh"
 
 namespace wqmm {
 namespace {
 
-// ------------------------------------------------------------------ shrink
-// A CTA has BM rows and one of the cluster's shares of the contraction; the
-// shares' sums meet in the cluster's shared memory, always in the order of the
-// CTAs.  WM warps split the rows (16 each); with WM == 1 the four warps split
-// the contraction's 16-wide steps instead.
-template <int RT, bool KM, int BM>
-struct ShrinkSmem {
-  static constexpr int RP = RT * 16;
-  static constexpr int kX = BM * 128;
-  static constexpr int kWPitch = KM ? 128 : RP * 2 + 16;
-  static constexpr int kW = KM ? RP * 128 : 64 * kWPitch;
-  static constexpr int kStage = kX + kW;
-  static constexpr int kStages = 4;
-  static constexpr int kBytes = kStage * kStages;
-};
-
-// Few rows, k-major weights: nothing is shared between the warps, so the
-// matrix instruction's operands come straight from global memory.  A thread
-// loads 16 bytes of its rows and of its weight rows, eight neighbours of the
-// contraction; four threads' 32 make two steps of the instruction.  Which
-// element stands for which of a step's sixteen does not matter to the sum as
-// long as both operands agree.  Each warp takes every fourth 32.
-template <bool BF16, int RT>
-__device__ __forceinline__ void few_rows_sum(const LoraRows& rows, const ShrinkParams& p, int rank, const Tile& tile,
-                                             int k0, int k1, float (&acc)[RT * 2][4]) {
-  constexpr int NT = RT * 2;
-  constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;  // 32s in flight: 16 to 18 loads
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const uint16_t* x[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t r = row_at(rows, tile.p0 + g + 8 * i, tile.p1);
-    x[i] = r >= 0 ? p.x.p + r * p.x.ld + q * 8 : nullptr;
-  }
-  const uint16_t* w = p.w + (static_cast<int64_t>(tile.group) * rank + g) * p.len + q * 8;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int k = k0 + warp * 32; k < k1; k += 128 * U) {
-    uint4 xv[U][2], wv[U][NT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = k + u * 128;
-      const bool in = at < k1;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        wv[u][n] = in && n * 8 < rank
-                       ? *reinterpret_cast<const uint4*>(w + static_cast<int64_t>(n) * 8 * p.len + at) : zero;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) xv[u][i] = in && x[i] ? *reinterpret_cast<const uint4*>(x[i] + at) : zero;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t a0[4] = {xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y};
-      const uint32_t a1[4] = {xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w};
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        mma<BF16>(acc[n], a0, wv[u][n].x, wv[u][n].y);
-        mma<BF16>(acc[n], a1, wv[u][n].z, wv[u][n].w);
-      }
-    }
-  }
-}
-
-template <bool BF16, int RT, bool KM, int WM>
-__device__ __forceinline__ void shrink_tile(const LoraRows& rows, const ShrinkParams& p, int rank, int cs,
-                                            const Tile& tile, uint8_t* sm) {
-  constexpr int RP = RT * 16, NT = RT * 2, BM = WM * 16;
-  using L = ShrinkSmem<RT, KM, BM>;
-  constexpr int S = L::kStages;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t base = smem_u32(sm);
-  const int crank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int steps_all = (p.len + 63) / 64;
-  const int s0 = static_cast<int>(static_cast<int64_t>(steps_all) * crank / cs);
-  const int s1 = static_cast<int>(static_cast<int64_t>(steps_all) * (crank + 1) / cs);
-  float acc[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-  const int wrow = WM == 1 ? 0 : warp * 16;
-  if constexpr (WM == 1 && KM) {
-    few_rows_sum<BF16, RT>(rows, p, rank, tile, s0 * 64, min(s1 * 64, p.len), acc);
-  } else {
-  const uint16_t* w = p.w + static_cast<int64_t>(tile.group) * rank * p.len;
-
-  // this thread's rows of x: 16-byte chunk tid % 8 of rows tid / 8 + 16 i
-  constexpr int XI = BM / 16;
-  const int xc = tid & 7;
-  const uint16_t* xrow[XI];
-  bool xhas[XI];
-#pragma unroll
-  for (int i = 0; i < XI; ++i) {
-    const int64_t r = row_at(rows, tile.p0 + tid / 8 + 16 * i, tile.p1);
-    xhas[i] = r >= 0;
-    xrow[i] = p.x.p + (r >= 0 ? r * p.x.ld : 0);
-  }
-  auto load = [&](int step, int stage) {
-    const uint32_t xs = base + stage * L::kStage, ws = xs + L::kX;
-    const int k = step * 64 + xc * 8;
-#pragma unroll
-    for (int i = 0; i < XI; ++i) {
-      const int r = tid / 8 + 16 * i;
-      const bool has = xhas[i] && k < p.len;
-      cp16(xs + r * 128 + ((xc ^ (r & 7)) * 16), has ? xrow[i] + k : p.x.p, has);
-    }
-    if constexpr (KM) {
-#pragma unroll
-      for (int i = 0; i < RP / 16; ++i) {
-        const int r = tid / 8 + 16 * i;
-        const bool has = r < rank && k < p.len;
-        cp16(ws + r * 128 + ((xc ^ (r & 7)) * 16), has ? w + static_cast<int64_t>(r) * p.len + k : w, has);
-      }
-    } else {
-      constexpr int C = RP / 8;  // chunks of a row
-#pragma unroll
-      for (int i = 0; i < 64 * C / kThreads; ++i) {
-        const int at = tid + i * kThreads, r = at / C, c = at % C, kk = step * 64 + r;
-        const bool has = kk < p.len && c * 8 < rank;
-        cp16(ws + r * L::kWPitch + c * 16, has ? w + static_cast<int64_t>(kk) * rank + c * 8 : w, has);
-      }
-    }
-  };
-
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) {
-    if (s0 + i < s1) load(s0 + i, i);
-    cp_async_commit();
-  }
-  for (int st = s0; st < s1; ++st) {
-    cp_async_wait_group<S - 2>();
-    __syncthreads();
-    if (st + S - 1 < s1) load(st + S - 1, (st - s0 + S - 1) % S);
-    cp_async_commit();
-    const uint32_t xs = base + ((st - s0) % S) * L::kStage, ws = xs + L::kX;
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      if (WM == 1 && kk != warp) continue;
-      uint32_t a[4];
-      {
-        const int r = wrow + (lane & 15), c = kk * 2 + (lane >> 4);
-        ldsm4(a, xs + r * 128 + ((c ^ (r & 7)) * 16));
-      }
-#pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        uint32_t b[4];
-        if constexpr (KM) {
-          const int r = n * 8 + ((lane >> 4) << 3) + (lane & 7), c = kk * 2 + ((lane >> 3) & 1);
-          ldsm4(b, ws + r * 128 + ((c ^ (r & 7)) * 16));
-        } else {
-          const int r = kk * 16 + (lane & 15), c = n + (lane >> 4);
-          ldsm4t(b, ws + r * L::kWPitch + c * 16);
-        }
-        mma<BF16>(acc[n], a, b[0], b[1]);
-        mma<BF16>(acc[n + 1], a, b[2], b[3]);
-      }
-    }
-  }
-  cp_async_wait_group<0>();
-  __syncthreads();
-
-  }
-
-  // sums to shared memory, [row][RP]; with WM == 1 the warps' behind it first
-  float* red = reinterpret_cast<float*>(sm);
-  {
-    float* mine = red + (WM == 1 ? (1 + warp) * 16 * RP : wrow * RP);
-    const int g = lane >> 2, q = lane & 3;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      *reinterpret_cast<float2*>(mine + g * RP + n * 8 + 2 * q) = make_float2(acc[n][0], acc[n][1]);
-      *reinterpret_cast<float2*>(mine + (g + 8) * RP + n * 8 + 2 * q) = make_float2(acc[n][2], acc[n][3]);
-    }
-  }
-  if constexpr (WM == 1) {
-    __syncthreads();
-    for (int at = tid; at < 16 * RP; at += kThreads)
-      red[at] = (red[16 * RP + at] + red[32 * RP + at]) + (red[48 * RP + at] + red[64 * RP + at]);
-  }
-  if (cs > 1)
-    cluster_sync();
-  else
-    __syncthreads();
-
-  // four values of a row per lane; the CTAs of the cluster share the rows
-  constexpr int LANES = RP / 4, PER = kThreads / LANES;
+// ------------------------------------------------------------------ the shares' sums
+// A tile of rows is shared by the CTAs of a cluster, each with a part of the
+// contraction and its sums [BM][PITCH] in shared memory at `red`.  The CTAs deal
+// the rows among themselves and add the parts in the order of the CTAs, so the
+// result does not depend on timing.  Then scale, the row's power of two
+// (float16) and the two 16-bit numbers.  Called by kThreads threads, tid 0 ...
+template <bool BF16, int RT, int BM, int PITCH>
+__device__ __forceinline__ void finish_rows(const ShrinkParams& p, const Tile& tile, const float* red, int cs,
+                                            int crank, int tid) {
+  constexpr int RP = RT * 16;
+  constexpr int LANES = RP / 4, PER = kThreads / LANES;  // four values of a row per lane
   const int sub = tid % LANES;
   const float scale = p.scale ? p.scale[tile.group] : 1.f;
   for (int r0 = crank * PER; r0 < BM; r0 += cs * PER) {
@@ -197,7 +23,7 @@ __device__ __forceinline__ void shrink_tile(const LoraRows& rows, const ShrinkPa
     const bool live = r < BM && place < tile.p1;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (live) {
-      const uint32_t at = smem_u32(red + r * RP + sub * 4);
+      const uint32_t at = smem_u32(red + r * PITCH + sub * 4);
       float4 f[8];  // all CTAs' parts in flight at once
 #pragma unroll
       for (int c = 0; c < 8; ++c)
@@ -250,60 +76,409 @@ __device__ __forceinline__ void shrink_tile(const LoraRows& rows, const ShrinkPa
       *reinterpret_cast<uint2*>(o + RP) = make_uint2(lo[0], lo[1]);
     }
   }
+}
+
+// ------------------------------------------------------------------ few rows
+// Tiles of 16 rows: the four warps split the contraction.
+
+// Few rows, k-major weights: nothing is shared between the warps, so the
+// matrix instruction's operands come straight from global memory.  A thread
+// loads 16 bytes of its rows and of its weight rows, eight neighbours of the
+// contraction; four threads' 32 make two steps of the instruction.  Which
+// element stands for which of a step's sixteen does not matter to the sum as
+// long as both operands agree.  Each warp takes every fourth 32.
+template <bool BF16, int RT>
+__device__ __forceinline__ void few_rows_sum(const LoraRows& rows, const ShrinkParams& p, int rank, const Tile& tile,
+                                             int k0, int k1, float (&acc)[RT * 2][4]) {
+  constexpr int NT = RT * 2;
+  constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;  // 32s in flight: 16 to 18 loads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const uint16_t* x[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t r = row_at(rows, tile.p0 + g + 8 * i, tile.p1);
+    x[i] = r >= 0 ? p.x.p + r * p.x.ld + q * 8 : nullptr;
+  }
+  const uint16_t* w = p.w + (static_cast<int64_t>(tile.group) * rank + g) * p.len + q * 8;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int k = k0 + warp * 32; k < k1; k += 128 * U) {
+    uint4 xv[U][2], wv[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = k + u * 128;
+      const bool in = at < k1;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        wv[u][n] = in && n * 8 < rank
+                       ? *reinterpret_cast<const uint4*>(w + static_cast<int64_t>(n) * 8 * p.len + at) : zero;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) xv[u][i] = in && x[i] ? *reinterpret_cast<const uint4*>(x[i] + at) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t a0[4] = {xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y};
+      const uint32_t a1[4] = {xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma<BF16>(acc[n], a0, wv[u][n].x, wv[u][n].y);
+        mma<BF16>(acc[n], a1, wv[u][n].z, wv[u][n].w);
+      }
+    }
+  }
+}
+
+// Rank-major weights are staged in shared memory, 64 steps of the contraction at
+// a time, so that the transposing load can make the instruction's operand of them.
+template <int RT>
+struct FewSmem {
+  static constexpr int RP = RT * 16;
+  static constexpr int kX = 16 * 128;
+  static constexpr int kWPitch = RP * 2 + 16;
+  static constexpr int kStage = kX + 64 * kWPitch;
+  static constexpr int kStages = 4;
+  static constexpr int kRed = 80 * RP * 4;  // the tile's sums, and the four warps' behind them
+};
+
+template <bool BF16, int RT>
+__device__ __forceinline__ void few_rows_staged_sum(const LoraRows& rows, const ShrinkParams& p, int rank,
+                                                    const Tile& tile, int s0, int s1, uint8_t* sm,
+                                                    float (&acc)[RT * 2][4]) {
+  constexpr int RP = RT * 16, NT = RT * 2;
+  using L = FewSmem<RT>;
+  constexpr int S = L::kStages;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = smem_u32(sm);
+  const uint16_t* w = p.w + static_cast<int64_t>(tile.group) * rank * p.len;
+  // this thread's part of x: 16-byte chunk tid % 8 of row tid / 8
+  const int xc = tid & 7, xr = tid / 8;
+  const int64_t row = row_at(rows, tile.p0 + xr, tile.p1);
+  const uint16_t* x = p.x.p + (row >= 0 ? row * p.x.ld : 0);
+  auto load = [&](int step, int stage) {
+    const uint32_t xs = base + stage * L::kStage, ws = xs + L::kX;
+    const int k = step * 64 + xc * 8;
+    const bool xhas = row >= 0 && k < p.len;
+    cp16(xs + xr * 128 + ((xc ^ (xr & 7)) * 16), xhas ? x + k : p.x.p, xhas);
+    constexpr int C = RP / 8;  // chunks of a row
+#pragma unroll
+    for (int i = 0; i < 64 * C / kThreads; ++i) {
+      const int at = tid + i * kThreads, r = at / C, c = at % C, kk = step * 64 + r;
+      const bool has = kk < p.len && c * 8 < rank;
+      cp16(ws + r * L::kWPitch + c * 16, has ? w + static_cast<int64_t>(kk) * rank + c * 8 : w, has);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) {
+    if (s0 + i < s1) load(s0 + i, i);
+    cp_async_commit();
+  }
+  for (int st = s0; st < s1; ++st) {
+    cp_async_wait_group<S - 2>();
+    __syncthreads();
+    if (st + S - 1 < s1) load(st + S - 1, (st - s0 + S - 1) % S);
+    cp_async_commit();
+    const uint32_t xs = base + ((st - s0) % S) * L::kStage, ws = xs + L::kX;
+    uint32_t a[4];
+    const int r = lane & 15, c = warp * 2 + (lane >> 4);
+    ldsm4(a, xs + r * 128 + ((c ^ (r & 7)) * 16));
+#pragma unroll
+    for (int n = 0; n < NT; n += 2) {
+      uint32_t b[4];
+      ldsm4t(b, ws + (warp * 16 + (lane & 15)) * L::kWPitch + (n + (lane >> 4)) * 16);
+      mma<BF16>(acc[n], a, b[0], b[1]);
+      mma<BF16>(acc[n + 1], a, b[2], b[3]);
+    }
+  }
+  cp_async_wait_group<0>();
+  __syncthreads();
+}
+
+template <bool BF16, int RT, bool KM>
+__device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const ShrinkParams& p, int rank, int cs,
+                                              const Tile& tile, uint8_t* sm) {
+  constexpr int RP = RT * 16, NT = RT * 2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int crank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int steps = (p.len + 63) / 64;
+  const int s0 = static_cast<int>(static_cast<int64_t>(steps) * crank / cs);
+  const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (crank + 1) / cs);
+  float acc[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+  if constexpr (KM)
+    few_rows_sum<BF16, RT>(rows, p, rank, tile, s0 * 64, min(s1 * 64, p.len), acc);
+  else
+    few_rows_staged_sum<BF16, RT>(rows, p, rank, tile, s0, s1, sm, acc);
+
+  float* red = reinterpret_cast<float*>(sm);
+  {
+    float* mine = red + (1 + warp) * 16 * RP;
+    const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      *reinterpret_cast<float2*>(mine + g * RP + n * 8 + 2 * q) = make_float2(acc[n][0], acc[n][1]);
+      *reinterpret_cast<float2*>(mine + (g + 8) * RP + n * 8 + 2 * q) = make_float2(acc[n][2], acc[n][3]);
+    }
+  }
+  __syncthreads();
+  for (int at = tid; at < 16 * RP; at += kThreads)
+    red[at] = (red[16 * RP + at] + red[32 * RP + at]) + (red[48 * RP + at] + red[64 * RP + at]);
+  if (cs > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  finish_rows<BF16, RT, 16, RP>(p, tile, red, cs, crank, tid);
   if (cs > 1) cluster_sync();  // no CTA ends while another reads its sums
 }
 
-template <bool BF16, int RT, int WM, bool BOTH>
-__global__ void __launch_bounds__(kThreads) shrink_kernel(LoraRows rows, ShrinkParams p0, ShrinkParams p1, int rank,
-                                                          int cs) {
+template <bool BF16, int RT, bool BOTH>
+__global__ void __launch_bounds__(kThreads) shrink_few_kernel(LoraRows rows, ShrinkParams p0, ShrinkParams p1,
+                                                              int rank, int cs) {
   extern __shared__ __align__(128) uint8_t sm[];
   pdl_wait();
   pdl_trigger();
   Tile tile;
-  if (!find_tile(rows, 0, WM * 16, blockIdx.x / cs, tile)) return;  // the same for the whole cluster
+  if (!find_tile(rows, 0, 16, blockIdx.x / cs, tile)) return;  // the same for the whole cluster
   if (!BOTH || blockIdx.y == 0)
-    shrink_tile<BF16, RT, true, WM>(rows, p0, rank, cs, tile, sm);
+    few_rows_tile<BF16, RT, true>(rows, p0, rank, cs, tile, sm);
   else
-    shrink_tile<BF16, RT, false, WM>(rows, p1, rank, cs, tile, sm);
+    few_rows_tile<BF16, RT, false>(rows, p1, rank, cs, tile, sm);
 }
 
-template <bool BF16, int RT, int WM, bool BOTH>
-cudaError_t shrink_as(const LoraRows& rows, const ShrinkParams* p, int rank, int sms, cudaStream_t s) {
-  constexpr int BM = WM * 16;
-  const int64_t tiles = most_tiles(rows.m, rows.adapters, BM);
-  const int len = BOTH ? std::max(p[0].len, p[1].len) : p[0].len;
-  // shares of the contraction: as many as fill the SMs four times over, each of at least four steps of 64
+// ------------------------------------------------------------------ many rows
+// Tiles of 128 rows on the tensor cores: D[128 rows][RP] += x[128][64] W[64][RP]
+// in steps of 64 of the contraction.  One warp gathers the rows of x (in the
+// order of their adapters) with tensor copies, one issues the MMAs, and four
+// read the sums at the end; nothing passes through registers on the way.  A
+// k-major W is K-major for the MMA, a rank-major one MN-major.
+template <int RT>
+struct ShrinkTc {
+  static constexpr int RP = RT * 16;
+  static constexpr int kX = 128 * 128, kW = RP * 128;
+  static constexpr int kStage = kX + kW;
+  static constexpr int kStages = RT == 1 ? 6 : RT == 2 ? 5 : RT == 4 ? 4 : 3;  // two CTAs per SM
+  static constexpr int kPitch = RP + 4;  // of the sums, floats: rows a bank group apart
+  static constexpr int kBytes = kStage * kStages + 1024;
+  static constexpr uint32_t kCols = RP < 32 ? 32 : RP;
+  static_assert(128 * kPitch * 4 <= kStage * kStages, "the sums reuse the stages");
+};
+
+template <bool BF16, int RT, bool BOTH>
+__global__ void __launch_bounds__(kTcThreads) shrink_tc_kernel(LoraRows rows, ShrinkParams p0, ShrinkParams p1,
+                                                               const __grid_constant__ TcMaps maps, int cs,
+                                                               uint32_t* err) {
+  using L = ShrinkTc<RT>;
+  using W = RankRows<RT>;
+  constexpr int S = L::kStages, RP = L::RP;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t full[S], empty[S], done;
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_sh;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool km = !BOTH || blockIdx.y == 0;
+  const ShrinkParams& p = km ? p0 : p1;
+  const CUtensorMap* xmap = &maps.x[km ? 0 : 1];
+  const CUtensorMap* wmap = &maps.w[km ? 0 : 1];
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(xmap);
+    prefetch_tensormap(wmap);
+  }
+  pdl_wait();
+  pdl_trigger();
+  Tile tile;
+  if (!find_tile(rows, 0, 128, blockIdx.x / cs, tile)) return;  // the same for the whole cluster
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&done, 1);
+    abort_sh = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_sh, L::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  volatile int* abort = &abort_sh;
+  const int crank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int steps = (p.len + 63) / 64;
+  const int s0 = static_cast<int>(static_cast<int64_t>(steps) * crank / cs);
+  const int n = static_cast<int>(static_cast<int64_t>(steps) * (crank + 1) / cs) - s0;  // this CTA's steps
+  const uint32_t base = smem_u32(sm);
+
+  if (warp == 0) {
+    // rows 4 * lane .. + 3 of the tile; four that are all outside are not copied
+    int r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t v = row_at(rows, tile.p0 + 4 * lane + i, tile.p1);
+      r[i] = static_cast<int>(v >= 0 ? v : rows.m);  // the row behind the last reads as zeros
+    }
+    const int4 four = make_int4(r[0], r[1], r[2], r[3]);
+    const bool any = tile.p0 + 4 * lane < tile.p1;
+    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, any)) * 512 + W::kBytes;
+    int i = 0;
+    for (; i < n; ++i) {
+      const int st = i % S;
+      if (i >= S && !warp_wait(&empty[st], ((i / S) & 1) ^ 1, abort, err, kDevTimeoutProducer)) break;
+      const uint32_t xs = base + st * L::kStage, ws = xs + L::kX;
+      const int k = (s0 + i) * 64;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[st], bytes);
+        if (km) {
+          tma_load_3d(ws, wmap, &full[st], k, 0, tile.group);
+        } else {
+#pragma unroll
+          for (int b = 0; b < W::kBlocks; ++b)
+            tma_load_3d(ws + b * W::kBlock, wmap, &full[st], b * W::kCols, k, tile.group);
+        }
+      }
+      __syncwarp();
+      if (any) tma_gather4(xs + lane * 512, xmap, &full[st], k, four);
+      __syncwarp();
+    }
+    if (lane == 0)  // every copy issued lands before the CTA may end
+      for (int j = i > S ? i - S : 0; j < i; ++j) {
+        volatile int no_abort = 0;
+        mbar_wait(&full[j % S], (j / S) & 1, &no_abort, err, kDevTimeoutDrain);
+      }
+    __syncwarp();
+  } else if (warp == 1) {
+    constexpr uint32_t kIdesc = idesc_make(1u, BF16 ? 1u : 0u, 128, RP);
+    constexpr uint64_t kKBits = operand_bits(128, 16, 1024);
+    for (int i = 0; i < n; ++i) {
+      const int st = i % S;
+      if (!warp_wait(&full[st], (i / S) & 1, abort, err, kDevTimeoutMma)) break;
+      tc_fence_after();
+      const uint32_t xs = base + st * L::kStage, ws = xs + L::kX;
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t a = operand(xs + k * 32, kKBits);
+          if (km)
+            mma_f16_ss(tmem, a, operand(ws + k * 32, kKBits), kIdesc, i > 0 || k > 0);
+          else
+            mma_f16_ss(tmem, a, operand(ws + k * W::kStep, W::kBits), kIdesc | kBMn, i > 0 || k > 0);
+        }
+        mma_commit(&empty[st]);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) mma_commit(&done);
+    __syncwarp();
+    volatile int no_abort = 0;
+    warp_wait(&done, 0, &no_abort, err, kDevTimeoutDrain);
+  }
+  __syncthreads();  // the MMAs are done, and nothing of the stages is read or written any more
+
+  float* red = reinterpret_cast<float*>(sm);
+  if (warp >= 2) {
+    tc_fence_after();
+    const int quad = warp & 3;  // the lanes of tensor memory that this warp may read
+    float* mine = red + (quad * 32 + lane) * L::kPitch;
+#pragma unroll
+    for (int c = 0; c < RP; c += 16) {
+      uint32_t v[16];
+      if (n > 0) {
+        tmem_ld_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, v);
+        tmem_wait_ld_r16(v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<uint4*>(mine + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (cs > 1) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kCols);
+  }
+  if (warp >= 2) finish_rows<BF16, RT, 128, L::kPitch>(p, tile, red, cs, crank, threadIdx.x - 64);
+  __syncwarp();
+  if (cs > 1) cluster_sync();  // no CTA ends while another reads its sums
+}
+
+// ------------------------------------------------------------------ launches
+// Shares of a contraction of `len`: as many as give `want` CTAs, each of at
+// least four steps of 64.
+int shares(int64_t tiles, int len, int64_t want) {
   int cs = 1;
-  while (cs < 8 && tiles * (BOTH ? 2 : 1) * cs < 4 * sms && (len + 63) / 64 >= 8 * cs) cs *= 2;
-  size_t smem = WM == 1 ? 0 : ShrinkSmem<RT, true, BM>::kBytes;
-  if (BOTH) smem = std::max<size_t>(smem, ShrinkSmem<RT, false, BM>::kBytes);
-  smem = std::max<size_t>(smem, static_cast<size_t>(WM == 1 ? 80 : BM) * RT * 16 * 4);
-  auto kernel = shrink_kernel<BF16, RT, WM, BOTH>;
+  while (cs < 8 && tiles * cs < want && (len + 63) / 64 >= 8 * cs) cs *= 2;
+  return cs;
+}
+
+template <bool BF16, int RT, bool BOTH>
+cudaError_t shrink_few(const LoraRows& rows, const ShrinkParams* p, int rank, int sms, cudaStream_t s) {
+  const int64_t tiles = most_tiles(rows.m, rows.adapters, 16);
+  const int cs = shares(tiles * (BOTH ? 2 : 1), BOTH ? std::max(p[0].len, p[1].len) : p[0].len, 4 * sms);
+  size_t smem = FewSmem<RT>::kRed;
+  if (BOTH) smem = std::max<size_t>(smem, FewSmem<RT>::kStage * FewSmem<RT>::kStages);
+  auto kernel = shrink_few_kernel<BF16, RT, BOTH>;
   if (const cudaError_t e = allow_smem(kernel, smem); e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs), BOTH ? 2 : 1), dim3(kThreads), smem, cs, s, rows,
                     p[0], p[BOTH ? 1 : 0], rank, cs);
+}
+
+template <bool BF16, int RT, bool BOTH>
+cudaError_t shrink_many(const LoraRows& rows, const ShrinkParams* p, const TcMaps& maps, int sms, cudaStream_t s) {
+  const int64_t tiles = most_tiles(rows.m, rows.adapters, 128);
+  const int cs = shares(tiles * (BOTH ? 2 : 1), BOTH ? std::max(p[0].len, p[1].len) : p[0].len, 2 * sms);
+  auto kernel = shrink_tc_kernel<BF16, RT, BOTH>;
+  if (const cudaError_t e = allow_smem(kernel, ShrinkTc<RT>::kBytes); e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs), BOTH ? 2 : 1), dim3(kTcThreads),
+                    ShrinkTc<RT>::kBytes, cs, s, rows, p[0], p[BOTH ? 1 : 0], maps, cs, device_error_word());
+}
+
+// The maps of x (gathered rows) and of the weights of one contraction.
+wqmm_status shrink_maps(const LoraRows& rows, const ShrinkParams& p, int rank, bool rank_major, bool bf16,
+                        CUtensorMap* x, CUtensorMap* w) {
+  const uint64_t xe[2] = {static_cast<uint64_t>(p.len), static_cast<uint64_t>(rows.m)};
+  const uint64_t xs[1] = {static_cast<uint64_t>(p.x.ld) * 2};
+  const uint32_t xb[2] = {64, 1};
+  wqmm_status st = tensor_map16(x, p.x.p, bf16, 2, xe, xs, xb, 128);
+  if (st) return st;
+  const int rp = lora_padded_rank(rank);
+  const uint64_t in = rank_major ? rank : p.len, out = rank_major ? p.len : rank;
+  const uint64_t we[3] = {in, out, static_cast<uint64_t>(rows.adapters)};
+  const uint64_t ws[2] = {in * 2, in * out * 2};
+  const uint32_t cols = rank_major ? std::min(rp, 64) : 64;
+  const uint32_t wb[3] = {cols, static_cast<uint32_t>(rank_major ? 64 : rp), 1};
+  return tensor_map16(w, p.w, bf16, 3, we, ws, wb, static_cast<int>(cols) * 2);
 }
 
 }  // namespace
 
 int lora_padded_rank(int rank) { return 16 * padded_sixteenths(rank); }
 
-cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
+wqmm_status launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
                                cudaStream_t s) {
-  return with_rank(rank, [&](auto rt) {
+  TcMaps maps;
+  const bool few = few_rows(rows);
+  if (!few)
+    for (int i = 0; i < count; ++i)
+      if (const wqmm_status st = shrink_maps(rows, p[i], rank, i == 1, bf16, &maps.x[i], &maps.w[i])) return st;
+  const cudaError_t e = with_rank(rank, [&](auto rt) {
     constexpr int RT = decltype(rt)::value;
-    auto pick = [&](auto t, auto wm, auto both) {
-      return shrink_as<decltype(t)::value, RT, decltype(wm)::value, decltype(both)::value>(rows, p, rank, sms, s);
+    auto pick = [&](auto t, auto both) {
+      constexpr bool T = decltype(t)::value, B = decltype(both)::value;
+      return few ? shrink_few<T, RT, B>(rows, p, rank, sms, s) : shrink_many<T, RT, B>(rows, p, maps, sms, s);
     };
-    auto by_wm = [&](auto t, auto both) {
-      return few_rows(rows) ? pick(t, std::integral_constant<int, 1>(), both)
-                            : pick(t, std::integral_constant<int, 4>(), both);
-    };
-    auto by_count = [&](auto t) {
-      return count == 2 ? by_wm(t, std::true_type()) : by_wm(t, std::false_type());
-    };
+    auto by_count = [&](auto t) { return count == 2 ? pick(t, std::true_type()) : pick(t, std::false_type()); };
     return bf16 ? by_count(std::true_type()) : by_count(std::false_type());
   });
+  return e == cudaSuccess ? WQMM_SUCCESS : cuda_fail(e, "adapter contraction launch");
 }
 
 }  // namespace wqmm
