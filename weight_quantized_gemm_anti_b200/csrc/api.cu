@@ -821,35 +821,6 @@ wqmm_status make_tmap(CUtensorMap* map, const void* base, CUtensorMapDataType dt
   return WQMM_SUCCESS;
 }
 
-}  // namespace
-
-namespace wqmm {
-
-wqmm_status tensor_map16(CUtensorMap* map, const void* base, bool bf16, int dims, const uint64_t* extent,
-                         const uint64_t* stride_bytes, const uint32_t* box, int swizzle_bytes) {
-  EncodeFn fn = encode_fn();
-  if (!fn) return fail(WQMM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  cuuint64_t d[3], st[2];
-  cuuint32_t b[3], one[3] = {1, 1, 1};
-  for (int i = 0; i < dims; ++i) {
-    d[i] = extent[i];
-    b[i] = box[i];
-    if (i + 1 < dims) st[i] = stride_bytes[i];
-  }
-  const CUtensorMapSwizzle sw = swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                      : CU_TENSOR_MAP_SWIZZLE_32B;
-  const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims,
-                        const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(WQMM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
-  return WQMM_SUCCESS;
-}
-
-}  // namespace wqmm
-
-namespace {
-
 wqmm_status take_executor(wqmm_executor* ex, OpKind op) {
   if (!ex) return fail(WQMM_ERR_EXECUTOR, "executor is null");
   if (!is_live(ex) || ex->magic != kMagicLive)

@@ -2,7 +2,6 @@
 // units: error messages, descriptor checks, and executors whose plan lives
 // outside api.cu.  Not part of the public ABI.
 #pragma once
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -25,12 +24,6 @@ bool aligned16(const void* p);
 wqmm_status check_descriptor(const wqmm_tensor* t, const char* name);
 int sm_count();
 uint64_t round_up(uint64_t v, uint64_t a);
-
-// Tensor map of a 16-bit tensor of 2 or 3 dimensions, innermost first (its
-// elements are neighbours; `stride_bytes` of the others), for copies of `box`
-// in the given swizzle; what lies outside the extents reads as zeros.
-wqmm_status tensor_map16(CUtensorMap* map, const void* base, bool bf16, int dims, const uint64_t* extent,
-                         const uint64_t* stride_bytes, const uint32_t* box, int swizzle_bytes);
 
 enum class OpKind { kWqmm, kQmm, kRoute, kLora };
 

@@ -4,6 +4,7 @@
 // and lora_outer.cu.
 #include "lora.h"
 
+#include "host.h"
 #include "route.h"
 
 using namespace wqmm;
@@ -178,9 +179,10 @@ struct AddPlan final : OpPlan {
   wqmm_status run(void* workspace, cudaStream_t s) override {
     const LoraLow low = low_at(p, static_cast<uint8_t*>(workspace));
     const ShrinkParams sp[1] = {{p.x, p.a, p.scale, low, p.k}};
-    if (const wqmm_status st = launch_lora_shrink(p.rows, sp, 1, p.rank, p.bf16, sm_count(), s)) return st;
+    cudaError_t e = launch_lora_shrink(p.rows, sp, 1, p.rank, p.bf16, sm_count(), s);
+    if (e != cudaSuccess) return cuda_fail(e, "adapter contraction launch");
     const ExpandParams ep{low, p.b, y, out, ldo, p.n, y.p != out};
-    const cudaError_t e = launch_lora_expand(p.rows, ep, p.rank, false, p.bf16, sm_count(), s);
+    e = launch_lora_expand(p.rows, ep, p.rank, false, p.bf16, sm_count(), s);
     return e == cudaSuccess ? WQMM_SUCCESS : cuda_fail(e, "adapter expansion launch");
   }
 };
@@ -196,12 +198,14 @@ struct GradPlan final : OpPlan {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const LoraLow low = low_at(p, ws), back = low_at(p, ws + low_bytes(p));
     const ShrinkParams sp[2] = {{p.x, p.a, p.scale, low, p.k}, {grad, p.b, p.scale, back, p.n}};
-    if (const wqmm_status st = launch_lora_shrink(p.rows, sp, 2, p.rank, p.bf16, sm_count(), s)) return st;
+    cudaError_t e = launch_lora_shrink(p.rows, sp, 2, p.rank, p.bf16, sm_count(), s);
+    if (e != cudaSuccess) return cuda_fail(e, "adapter contraction launch");
     const OuterParams op[2] = {{p.x, back, ga, p.k, 1}, {grad, low, gb, p.n, 0}};
-    if (const wqmm_status st = launch_lora_outer(p.rows, op, p.rank, p.bf16, sm_count(), s)) return st;
+    e = launch_lora_outer(p.rows, op, p.rank, p.bf16, sm_count(), s);
+    if (e != cudaSuccess) return cuda_fail(e, "adapter weight gradient launch");
     if (gx) {
       const ExpandParams ep{back, p.a, gx_in, gx, ldgx, p.k, gx_in.p != gx};
-      const cudaError_t e = launch_lora_expand(p.rows, ep, p.rank, true, p.bf16, sm_count(), s);
+      e = launch_lora_expand(p.rows, ep, p.rank, true, p.bf16, sm_count(), s);
       if (e != cudaSuccess) return cuda_fail(e, "adapter input gradient launch");
     }
     return WQMM_SUCCESS;

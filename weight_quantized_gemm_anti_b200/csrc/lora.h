@@ -6,8 +6,6 @@
 
 #include <cstdint>
 
-#include "host.h"
-#include "internal.h"
 
 namespace wqmm {
 
@@ -62,11 +60,11 @@ struct OuterParams {
 
 int lora_padded_rank(int rank);
 // x by x k-major weights, and with count 2 then by rank-major ones.
-wqmm_status launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
+cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
                                cudaStream_t s);
 cudaError_t launch_lora_expand(const LoraRows& rows, const ExpandParams& p, int rank, bool rank_major, bool bf16,
                                int sms, cudaStream_t s);
-wqmm_status launch_lora_outer(const LoraRows& rows, const OuterParams (&p)[2], int rank, bool bf16, int sms,
+cudaError_t launch_lora_outer(const LoraRows& rows, const OuterParams (&p)[2], int rank, bool bf16, int sms,
                               cudaStream_t s);
 
 }  // namespace wqmm

@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "internal.h"
 #include "launch.cuh"
 #include "lora.h"
 #include "ptx.cuh"

@@ -9,18 +9,16 @@ namespace {
 // row of low lie along the contraction as they are in memory.  low's two
 // 16-bit numbers are two MMAs into the same sums.
 //
-// Roles: one warp gathers the rows of x (in the order of their adapters) and
-// copies low's; one issues the MMAs; four write the sums; four put the
-// operand low right where it is not as it was copied: rows behind the
-// adapter's last belong to another one and become zeros (what they hold may
-// not be finite), and float16 rows, whose powers of two differ, are brought to
-// the largest of the CTA's rows.
+// Roles: four warps copy the rows of x (in the order of their adapters) and of
+// low, one issues the MMAs, four write the sums.  Rows behind the adapter's last
+// are zeros in both operands.  float16 rows of low have a power of two each;
+// on their way to shared memory they are brought to the largest of the CTA's rows.
 //
 // An item is 128 columns of one adapter's gradient.  With few items a cluster
 // shares one, each CTA a part of the rows, and the parts meet in shared memory
 // in the order of the CTAs; with many a CTA goes through several, the copies of
 // the next under way while one is written (its sums are in tensor memory twice).
-constexpr int kOuterThreads = 320;
+constexpr int kOuterThreads = kCopyThreads + 128 + 32;
 
 template <int RT>
 struct OuterTc {
@@ -36,11 +34,6 @@ struct OuterTc {
   static_assert(128 * kPitch * 4 <= kStage * kStages, "the sums reuse the stages");
 };
 
-struct OuterMaps {
-  CUtensorMap x[2];    // gathered rows: box 64 columns x 1 row, 128-byte swizzle
-  CUtensorMap low[2];  // box 64 rows
-};
-
 // Two neighbours of the gradient: columns c (and c + 1 in the rank-row form), rank rows r (and r + 1 otherwise).
 template <bool BF16>
 __device__ __forceinline__ void put_pair(uint16_t* out, const OuterParams& p, int rank, int c, int r, float a, float b) {
@@ -50,28 +43,26 @@ __device__ __forceinline__ void put_pair(uint16_t* out, const OuterParams& p, in
 
 template <bool BF16, int RT>
 __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, OuterParams p0, OuterParams p1,
-                                                                 const __grid_constant__ OuterMaps maps, int rank,
-                                                                 int cs, int tiles0, int tiles, int items,
+                                                                 int rank, int cs, int tiles0, int tiles, int items,
                                                                  uint32_t* err) {
   using L = OuterTc<RT>;
   using R = RankRows<RT>;
-  constexpr int S = L::kStages, RP = L::RP;
+  constexpr int S = L::kStages, RP = L::RP, LAG = S - 2;  // LAG: steps under way behind the newest
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t full[S], right[S], empty[S], sums_full[2], sums_empty[2], top_ready[2], done;
+  __shared__ __align__(8) uint64_t full[S], empty[S], sums_full[2], sums_empty[2], top_ready[2], done;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   __shared__ float top_sh[2], tops[4];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = smem_u32(sm);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int crank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int first = blockIdx.x / cs, stride = gridDim.x / cs;
 
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 4);
       mbar_init(&empty[i], 1);
-      mbar_init(&right[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sums_full[i], 1);
@@ -82,14 +73,12 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     abort_sh = 0;
     fence_barrier_init();
   }
-  __syncthreads();
   volatile int* abort = &abort_sh;
 
-  // an item's adapter, columns and steps; its rows are [r0, r1) in steps of 64 from r0 + 64 s0
+  // an item's adapter, columns and steps; its rows are [r0, r1), this CTA's those from `begin` in n steps of 64
   struct Item {
-    int which, c0, adapter;
-    int64_t r0, r1, s0;
-    int n;
+    int which, c0, adapter, n;
+    int64_t begin, r1;
   };
   auto item_at = [&](int it) {
     Item o;
@@ -97,58 +86,98 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     const int ct = it % tiles;
     o.which = ct < tiles0 ? 0 : 1;
     o.c0 = (ct < tiles0 ? ct : ct - tiles0) * 128;
-    o.r0 = offset_at(rows, o.adapter);
-    o.r1 = max(offset_at(rows, o.adapter + 1), o.r0);
-    const int64_t steps = (o.r1 - o.r0 + 63) / 64;
-    o.s0 = steps * crank / cs;
-    o.n = static_cast<int>(steps * (crank + 1) / cs - o.s0);
+    const int64_t r0 = offset_at(rows, o.adapter);
+    o.r1 = max(offset_at(rows, o.adapter + 1), r0);
+    const int64_t steps = (o.r1 - r0 + 63) / 64;
+    const int64_t s0 = steps * crank / cs;
+    o.begin = r0 + s0 * 64;
+    o.n = static_cast<int>(steps * (crank + 1) / cs - s0);
     return o;
   };
-  // The copy warp's part: four rows of x per lane and step, and low's rows.
-  const int quad4 = 4 * (lane & 15);
-  int64_t next[4];
+
+  // The copies of a step.  x: chunk tid % 16 (16 bytes) of rows tid / 16 + 8 i.  A warp has the sixteen rows
+  // 2 * warp + {0, 1} + 8 i; lane j holds the number of row j % 2 + 8 (j / 2) of them, loaded a step ahead.
+  const int xc = tid & 15, xr = (tid >> 4) & 7;
+  const uint32_t xto = (xc >> 3) * 8192 + swizzled<128>(xr, xc & 7);
+  int number = -1;
   auto find = [&](const Item& o, int i) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) next[j] = i < o.n ? row_at(rows, o.r0 + (o.s0 + i) * 64 + quad4 + j, o.r1) : -1;
+    const int64_t place = o.begin + i * 64 + 2 * (warp & 3) + (lane & 1) + 8 * ((lane & 15) >> 1);
+    number = i < o.n && place < o.r1 ? rows.source[place] : -1;
   };
   auto copy_x = [&](const Item& o, int st) {
-    int4 four;  // the row behind the last reads as zeros
-    four.x = static_cast<int>(next[0] >= 0 ? next[0] : rows.m);
-    four.y = static_cast<int>(next[1] >= 0 ? next[1] : rows.m);
-    four.z = static_cast<int>(next[2] >= 0 ? next[2] : rows.m);
-    four.w = static_cast<int>(next[3] >= 0 ? next[3] : rows.m);
-    if (lane == 0) mbar_arrive_expect_tx(&full[st], L::kStage);
-    __syncwarp();
-    tma_gather4(base + st * L::kStage + (lane >> 4) * 8192 + (lane & 15) * 512, &maps.x[o.which], &full[st],
-                o.c0 + (lane >> 4) * 64, four);
-    __syncwarp();
-  };
-  auto copy_low = [&](const Item& o, int i, int st) {
-    if (lane == 0) {
-      const int r = static_cast<int>(o.r0 + (o.s0 + i) * 64);
+    const OuterParams& p = o.which == 0 ? p0 : p1;
+    const uint32_t to = base + st * L::kStage + xto;
+    const bool in = o.c0 + xc * 8 < p.len;
+    const uint16_t* x = p.x.p + o.c0 + xc * 8;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int b = 0; b < R::kBlocks; ++b)
-          tma_load_2d(sm + st * L::kStage + L::kX + h * L::kLow + b * R::kBlock, &maps.low[o.which], &full[st],
-                      h * RP + b * R::kCols, r);
+    for (int i = 0; i < 8; ++i) {
+      const int v = __shfl_sync(0xffffffffu, number, (lane >> 4) + 2 * i);
+      const bool has = in && v >= 0 && v < rows.m;
+      cp16(to + i * 1024, has ? x + v * p.x.ld : p.x.p, has);
     }
-    __syncwarp();
   };
+  // low: 16-byte chunk at % (4 RT) of row at / (4 RT), both numbers of a row side by side
+  constexpr int kLowChunks = 2 * RT;  // per thread
+  auto low_from = [&](const Item& o, int i, int j, bool& has) {
+    const int at = tid + j * kCopyThreads, r = at / (4 * RT), c = at % (4 * RT);
+    const int64_t place = o.begin + i * 64 + r;
+    has = i < o.n && place < o.r1;
+    const uint16_t* low = (o.which == 0 ? p0 : p1).low.low;
+    return has ? low + place * (2 * RP) + c * 8 : low;
+  };
+  auto low_to = [&](int st, int j) {
+    const int at = tid + j * kCopyThreads, r = at / (4 * RT), c = at % (4 * RT);
+    return st * L::kStage + L::kX + c / (2 * RT) * L::kLow + R::at(r, c % (2 * RT));
+  };
+  auto copy_low = [&](const Item& o, int i, int st) {  // bfloat16
+#pragma unroll
+    for (int j = 0; j < kLowChunks; ++j) {
+      bool has;
+      const uint16_t* from = low_from(o, i, j, has);
+      cp16(base + low_to(st, j), from, has);
+    }
+  };
+  uint4 held[BF16 ? 1 : kLowChunks];  // float16: the next step's low, and its rows' powers of two
+  float held_by[BF16 ? 1 : kLowChunks];
+  auto load_low = [&](const Item& o, int i, float below) {
+#pragma unroll
+    for (int j = 0; j < (BF16 ? 0 : kLowChunks); ++j) {
+      bool has;
+      const uint16_t* from = low_from(o, i, j, has);
+      held[j] = has ? *reinterpret_cast<const uint4*>(from) : make_uint4(0, 0, 0, 0);
+      held_by[j] =
+          has ? (o.which == 0 ? p0 : p1).low.factor[o.begin + i * 64 + (tid + j * kCopyThreads) / (4 * RT)] * below : 0.f;
+    }
+  };
+  auto store_low = [&](int st) {
+#pragma unroll
+    for (int j = 0; j < (BF16 ? 0 : kLowChunks); ++j) {
+      const __half2 by = __float2half2_rn(held_by[j]);
+      uint32_t w[4] = {held[j].x, held[j].y, held[j].z, held[j].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&w[k]), by);
+        w[k] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      *reinterpret_cast<uint4*>(sm + low_to(st, j)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  };
+
   // x and the order are older than the launch before this one, which has waited for all that came
-  // before it: the first stages' rows of x are read while it ends, low after that
+  // before it: the first steps' rows of x are read while it ends, low after that
   int early = 0;
-  if (warp == 0 && first < items) {
+  if (warp < 4 && first < items) {
     const Item o = item_at(first);
-    for (; early < S && early < o.n; ++early) {
-      find(o, early);
+    find(o, 0);
+    for (; early < LAG && early < o.n; ++early) {
       copy_x(o, early);
+      find(o, early + 1);
     }
   }
   pdl_wait();
   pdl_trigger();
   // tensor memory is taken now: the launch before this one may have held it all
-  if (warp == 1) {
+  if (warp == 8) {
     tmem_alloc(&tmem_sh, L::kCols);
     tmem_relinquish();
   }
@@ -157,32 +186,67 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
 
-  if (warp == 0) {
-    int g = 0;
+  if (warp < 4) {
+    // ---------------------------------------------------------------- copies
+    // (after a wait that gave up these warps still go through the items, for the barriers among them)
+    int g = 0, k = 0, handed = 0;  // steps begun, items, steps handed over
     bool live = true;
-    for (int it = first; it < items && live; it += stride) {
+    for (int it = first; it < items; it += stride, ++k) {
       const Item o = item_at(it);
-      const int had = it == first ? early : 0;
-      for (int i = 0; i < had; ++i, ++g) copy_low(o, i, g % S);
-      find(o, had);
-      for (int i = had; i < o.n; ++i, ++g) {
-        const int st = g % S;
-        if (g >= S && !warp_wait(&empty[st], ((g / S) & 1) ^ 1, abort, err, kDevTimeoutProducer)) {
-          live = false;
-          break;
+      float below = 1.f;
+      if constexpr (!BF16) {
+        // the largest power of two of this CTA's rows
+        const float* factor = (o.which == 0 ? p0 : p1).low.factor + o.begin;
+        const int n = static_cast<int>(min(static_cast<int64_t>(o.n) * 64, o.r1 - o.begin));
+        float top = 0.f;
+        for (int r = tid; r < n; r += kCopyThreads) top = fmaxf(top, factor[r]);
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        named_bar_sync(1, kCopyThreads);  // the last item's maxima are read
+        if (lane == 0) tops[warp] = top;
+        named_bar_sync(1, kCopyThreads);
+        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        if (!(top > 0.f)) top = 1.f;  // no rows
+        below = 1.f / top;            // of a power of two: exact
+        // the maximum of two items ago has been read when its sums have
+        live = live && (k < 2 || warp_wait(&sums_empty[k & 1], ((k / 2) & 1) ^ 1, abort, err, kDevTimeoutDequant));
+        if (live && tid == 0) {
+          top_sh[k & 1] = top;
+          mbar_arrive(&top_ready[k & 1]);
         }
-        copy_x(o, st);
-        copy_low(o, i, st);
-        find(o, i + 1);
+        load_low(o, 0, below);
+      }
+      const int had = it == first ? early : 0;
+      if (had == 0) find(o, 0);
+      for (int i = 0; i < o.n; ++i, ++g) {
+        const int st = g % S;
+        live = live && (g < S || warp_wait(&empty[st], ((g / S) & 1) ^ 1, abort, err, kDevTimeoutProducer));
+        if (!live) continue;
+        if (i >= had) {
+          copy_x(o, st);
+          find(o, i + 1);
+        }
+        if constexpr (BF16) {
+          copy_low(o, i, st);
+        } else {
+          store_low(st);
+          load_low(o, i + 1, below);
+        }
+        cp_async_commit();
+        if (handed <= g - LAG) {
+          cp_async_wait_group<LAG>();
+          hand_over(&full[handed++ % S]);
+        }
+      }
+      // the item's last steps are handed over now: its sums do not wait for the next item's copies
+      if (live) {
+        cp_async_wait_group<0>();
+        for (; handed < g; ++handed) hand_over(&full[handed % S]);
       }
     }
-    if (lane == 0)  // every copy issued lands before the CTA may end
-      for (int j = g > S ? g - S : 0; j < g; ++j) {
-        volatile int no_abort = 0;
-        mbar_wait(&full[j % S], (j / S) & 1, &no_abort, err, kDevTimeoutDrain);
-      }
-    __syncwarp();
-  } else if (warp == 1) {
+    cp_async_wait_group<0>();
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- MMAs
     constexpr uint32_t kIdesc = idesc_make(1u, BF16 ? 1u : 0u, 128, RP) | kAMn | kBMn;
     constexpr uint64_t kXBits = operand_bits(128, 8192, 1024);
     int g = 0, k = 0;
@@ -195,8 +259,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
       const uint32_t d = tmem + buf * RP;
       for (int i = 0; i < o.n; ++i, ++g) {
         const int st = g % S;
-        if (!warp_wait(&full[st], (g / S) & 1, abort, err, kDevTimeoutMma) ||
-            !warp_wait(&right[st], (g / S) & 1, abort, err, kDevTimeoutMma)) {
+        if (!warp_wait(&full[st], (g / S) & 1, abort, err, kDevTimeoutMma)) {
           live = false;
           break;
         }
@@ -221,75 +284,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     __syncwarp();
     volatile int no_abort = 0;
     warp_wait(&done, 0, &no_abort, err, kDevTimeoutDrain);
-  } else if (warp >= 6) {
-    // ---------------------------------------------------------------- low put right
-    // (after a wait that gave up these warps still go through the loop, for the barriers among them)
-    const int tid = threadIdx.x - 192;
-    int g = 0, k = 0;
-    bool live = true;
-    for (int it = first; it < items; it += stride, ++k) {
-      const Item o = item_at(it);
-      const LoraLow& low = o.which == 0 ? p0.low : p1.low;
-      const int64_t begin = o.r0 + o.s0 * 64;
-      const int n = static_cast<int>(min(static_cast<int64_t>(o.n) * 64, o.r1 - begin));  // rows
-      float below = 1.f;
-      if constexpr (!BF16) {
-        float top = 0.f;
-        for (int r = tid; r < n; r += 128) top = fmaxf(top, low.factor[begin + r]);
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-        named_bar_sync(1, 128);  // the last item's maxima are read
-        if (lane == 0) tops[warp - 6] = top;
-        named_bar_sync(1, 128);
-        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-        if (!(top > 0.f)) top = 1.f;  // no rows
-        below = 1.f / top;            // of a power of two: exact
-        // the maximum of two items ago has been read when its sums have
-        live = live && (k < 2 || warp_wait(&sums_empty[k & 1], ((k / 2) & 1) ^ 1, abort, err, kDevTimeoutDequant));
-        if (live && tid == 0) {
-          top_sh[k & 1] = top;
-          mbar_arrive(&top_ready[k & 1]);
-        }
-      }
-      for (int i = 0; i < o.n; ++i, ++g) {
-        const int st = g % S;
-        constexpr int kChunks = 2 * L::kLow / 16 / 128;  // 16-byte chunks per thread
-        float f[kChunks];
-        if constexpr (!BF16) {
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            const int r = i * 64 + (((tid + c * 128) * 16) % R::kBlock) / R::kRow;
-            f[c] = r < n ? low.factor[begin + r] * below : 0.f;
-          }
-        }
-        live = live && warp_wait(&full[st], (g / S) & 1, abort, err, kDevTimeoutDequant);
-        if (!live) continue;
-        if (!BF16 || (i + 1) * 64 > n) {
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            const int r = i * 64 + (((tid + c * 128) * 16) % R::kBlock) / R::kRow;
-            uint4* at = reinterpret_cast<uint4*>(sm + st * L::kStage + L::kX + (tid + c * 128) * 16);
-            if (r >= n) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else if constexpr (!BF16) {
-              const __half2 by = __float2half2_rn(f[c]);
-              const uint4 v = *at;
-              uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __half2 x = __hmul2(*reinterpret_cast<__half2*>(&w[j]), by);
-                w[j] = *reinterpret_cast<const uint32_t*>(&x);
-              }
-              *at = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          fence_proxy_async_smem();  // the MMA reads what was written here
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&right[st]);
-      }
-    }
-  } else if (warp >= 2) {
+  } else {
     // ---------------------------------------------------------------- the sums
     const int quad = warp & 3;  // the lanes of tensor memory that this warp may read
     const int col = quad * 32 + lane;
@@ -348,7 +343,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     }
   }
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
   }
@@ -395,8 +390,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
 
 // ------------------------------------------------------------------ launches
 template <bool BF16, int RT>
-cudaError_t outer_as(const LoraRows& rows, const OuterParams (&p)[2], const OuterMaps& maps, int rank, int sms,
-                     cudaStream_t s) {
+cudaError_t outer_as(const LoraRows& rows, const OuterParams (&p)[2], int rank, int sms, cudaStream_t s) {
   using L = OuterTc<RT>;
   const int t0 = (p[0].len + 127) / 128, tiles = t0 + (p[1].len + 127) / 128;
   const int items = tiles * rows.adapters;
@@ -408,31 +402,17 @@ cudaError_t outer_as(const LoraRows& rows, const OuterParams (&p)[2], const Oute
   auto kernel = outer_tc_kernel<BF16, RT>;
   if (const cudaError_t e = allow_smem(kernel, L::kBytes); e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kOuterThreads), L::kBytes, cs, s, rows, p[0], p[1],
-                    maps, rank, cs, t0, tiles, items, device_error_word());
+                    rank, cs, t0, tiles, items, device_error_word());
 }
 
 }  // namespace
 
-wqmm_status launch_lora_outer(const LoraRows& rows, const OuterParams (&p)[2], int rank, bool bf16, int sms,
+cudaError_t launch_lora_outer(const LoraRows& rows, const OuterParams (&p)[2], int rank, bool bf16, int sms,
                               cudaStream_t s) {
-  OuterMaps maps;
-  const int rp = lora_padded_rank(rank);
-  for (int i = 0; i < 2; ++i) {
-    const uint64_t m = static_cast<uint64_t>(rows.m);
-    const uint64_t xe[2] = {static_cast<uint64_t>(p[i].len), m}, xs[1] = {static_cast<uint64_t>(p[i].x.ld) * 2};
-    const uint32_t xb[2] = {64, 1};
-    wqmm_status st = tensor_map16(&maps.x[i], p[i].x.p, bf16, 2, xe, xs, xb, 128);
-    if (st) return st;
-    const uint64_t le[2] = {static_cast<uint64_t>(2 * rp), m}, ls[1] = {static_cast<uint64_t>(4 * rp)};
-    const uint32_t lb[2] = {static_cast<uint32_t>(std::min(rp, 64)), 64};
-    st = tensor_map16(&maps.low[i], p[i].low.low, bf16, 2, le, ls, lb, static_cast<int>(lb[0]) * 2);
-    if (st) return st;
-  }
-  const cudaError_t e = with_rank(rank, [&](auto rt) {
+  return with_rank(rank, [&](auto rt) {
     constexpr int RT = decltype(rt)::value;
-    return bf16 ? outer_as<true, RT>(rows, p, maps, rank, sms, s) : outer_as<false, RT>(rows, p, maps, rank, sms, s);
+    return bf16 ? outer_as<true, RT>(rows, p, rank, sms, s) : outer_as<false, RT>(rows, p, rank, sms, s);
   });
-  return e == cudaSuccess ? WQMM_SUCCESS : cuda_fail(e, "adapter weight gradient launch");
 }
 
 }  // namespace wqmm

@@ -248,10 +248,9 @@ __global__ void __launch_bounds__(kThreads) shrink_few_kernel(LoraRows rows, Shr
 
 // ------------------------------------------------------------------ many rows
 // Tiles of 128 rows on the tensor cores: D[128 rows][RP] += x[128][64] W[64][RP]
-// in steps of 64 of the contraction.  One warp gathers the rows of x (in the
-// order of their adapters) with tensor copies, one issues the MMAs, and four
-// read the sums at the end; nothing passes through registers on the way.  A
-// k-major W is K-major for the MMA, a rank-major one MN-major.
+// in steps of 64 of the contraction.  Four warps copy x and W and read the sums
+// at the end, one issues the MMAs.  A k-major W is K-major for the MMA, a
+// rank-major one MN-major.
 template <int RT>
 struct ShrinkTc {
   static constexpr int RP = RT * 16;
@@ -263,11 +262,61 @@ struct ShrinkTc {
   static constexpr uint32_t kCols = RP < 32 ? 32 : RP;
   static_assert(128 * kPitch * 4 <= kStage * kStages, "the sums reuse the stages");
 };
+constexpr int kShrinkThreads = kCopyThreads + 32;
+
+template <bool BF16, int RT, bool KM>
+__device__ __forceinline__ void shrink_copies(const LoraRows& rows, const ShrinkParams& p, int rank, const Tile& tile,
+                                              int s0, int n, uint32_t base, uint64_t* full, uint64_t* empty,
+                                              volatile int* abort, uint32_t* err) {
+  using L = ShrinkTc<RT>;
+  constexpr int S = L::kStages, LAG = S - 2;  // steps under way behind the newest
+  const int tid = threadIdx.x;
+  const uint16_t* w = p.w + static_cast<int64_t>(tile.group) * rank * p.len;
+  // 16-byte chunk c of rows tid / 8 + 16 i of x (and of a k-major W)
+  const int c = tid & 7, r = tid >> 3;
+  const uint16_t* x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t v = row_at(rows, tile.p0 + r + 16 * i, tile.p1);
+    x[i] = v >= 0 ? p.x.p + v * p.x.ld : nullptr;
+  }
+  const uint32_t to = swizzled<128>(r, c);
+  int i = 0;
+  for (; i < n; ++i) {
+    const int st = i % S;
+    if (i >= S && !warp_wait(&empty[st], ((i / S) & 1) ^ 1, abort, err, kDevTimeoutProducer)) break;
+    const uint32_t xs = base + st * L::kStage, ws = xs + L::kX;
+    const int k = (s0 + i) * 64 + c * 8;
+    const bool in = k < p.len;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cp16(xs + to + j * 2048, in && x[j] ? x[j] + k : p.x.p, in && x[j]);
+    if constexpr (KM) {
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        const bool has = in && r + 16 * j < rank;
+        cp16(ws + to + j * 2048, has ? w + static_cast<int64_t>(r + 16 * j) * p.len + k : w, has);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        const int at = tid + j * kCopyThreads, wr = at / (2 * RT), wc = at % (2 * RT), kk = (s0 + i) * 64 + wr;
+        const bool has = kk < p.len && wc * 8 < rank;
+        cp16(ws + RankRows<RT>::at(wr, wc), has ? w + static_cast<int64_t>(kk) * rank + wc * 8 : w, has);
+      }
+    }
+    cp_async_commit();
+    if (i >= LAG) {
+      cp_async_wait_group<LAG>();
+      hand_over(&full[(i - LAG) % S]);
+    }
+  }
+  cp_async_wait_group<0>();
+  for (int j = i > LAG ? i - LAG : 0; j < i; ++j) hand_over(&full[j % S]);
+}
 
 template <bool BF16, int RT, bool BOTH>
-__global__ void __launch_bounds__(kTcThreads) shrink_tc_kernel(LoraRows rows, ShrinkParams p0, ShrinkParams p1,
-                                                               const __grid_constant__ TcMaps maps, int cs,
-                                                               uint32_t* err) {
+__global__ void __launch_bounds__(kShrinkThreads) shrink_tc_kernel(LoraRows rows, ShrinkParams p0, ShrinkParams p1,
+                                                                   int rank, int cs, uint32_t* err) {
   using L = ShrinkTc<RT>;
   using W = RankRows<RT>;
   constexpr int S = L::kStages, RP = L::RP;
@@ -279,26 +328,20 @@ __global__ void __launch_bounds__(kTcThreads) shrink_tc_kernel(LoraRows rows, Sh
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool km = !BOTH || blockIdx.y == 0;
   const ShrinkParams& p = km ? p0 : p1;
-  const CUtensorMap* xmap = &maps.x[km ? 0 : 1];
-  const CUtensorMap* wmap = &maps.w[km ? 0 : 1];
-  if (threadIdx.x == 0) {
-    prefetch_tensormap(xmap);
-    prefetch_tensormap(wmap);
-  }
-  pdl_wait();
-  pdl_trigger();
-  Tile tile;
-  if (!find_tile(rows, 0, 128, blockIdx.x / cs, tile)) return;  // the same for the whole cluster
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 4);
       mbar_init(&empty[i], 1);
     }
     mbar_init(&done, 1);
     abort_sh = 0;
     fence_barrier_init();
   }
-  if (warp == 1) {
+  pdl_wait();
+  pdl_trigger();
+  Tile tile;
+  if (!find_tile(rows, 0, 128, blockIdx.x / cs, tile)) return;  // the same for the whole cluster
+  if (warp == 4) {
     tmem_alloc(&tmem_sh, L::kCols);
     tmem_relinquish();
   }
@@ -313,44 +356,12 @@ __global__ void __launch_bounds__(kTcThreads) shrink_tc_kernel(LoraRows rows, Sh
   const int n = static_cast<int>(static_cast<int64_t>(steps) * (crank + 1) / cs) - s0;  // this CTA's steps
   const uint32_t base = smem_u32(sm);
 
-  if (warp == 0) {
-    // rows 4 * lane .. + 3 of the tile; four that are all outside are not copied
-    int r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t v = row_at(rows, tile.p0 + 4 * lane + i, tile.p1);
-      r[i] = static_cast<int>(v >= 0 ? v : rows.m);  // the row behind the last reads as zeros
-    }
-    const int4 four = make_int4(r[0], r[1], r[2], r[3]);
-    const bool any = tile.p0 + 4 * lane < tile.p1;
-    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, any)) * 512 + W::kBytes;
-    int i = 0;
-    for (; i < n; ++i) {
-      const int st = i % S;
-      if (i >= S && !warp_wait(&empty[st], ((i / S) & 1) ^ 1, abort, err, kDevTimeoutProducer)) break;
-      const uint32_t xs = base + st * L::kStage, ws = xs + L::kX;
-      const int k = (s0 + i) * 64;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[st], bytes);
-        if (km) {
-          tma_load_3d(ws, wmap, &full[st], k, 0, tile.group);
-        } else {
-#pragma unroll
-          for (int b = 0; b < W::kBlocks; ++b)
-            tma_load_3d(ws + b * W::kBlock, wmap, &full[st], b * W::kCols, k, tile.group);
-        }
-      }
-      __syncwarp();
-      if (any) tma_gather4(xs + lane * 512, xmap, &full[st], k, four);
-      __syncwarp();
-    }
-    if (lane == 0)  // every copy issued lands before the CTA may end
-      for (int j = i > S ? i - S : 0; j < i; ++j) {
-        volatile int no_abort = 0;
-        mbar_wait(&full[j % S], (j / S) & 1, &no_abort, err, kDevTimeoutDrain);
-      }
-    __syncwarp();
-  } else if (warp == 1) {
+  if (warp < 4) {
+    if (km)
+      shrink_copies<BF16, RT, true>(rows, p, rank, tile, s0, n, base, full, empty, abort, err);
+    else
+      shrink_copies<BF16, RT, false>(rows, p, rank, tile, s0, n, base, full, empty, abort, err);
+  } else {
     constexpr uint32_t kIdesc = idesc_make(1u, BF16 ? 1u : 0u, 128, RP);
     constexpr uint64_t kKBits = operand_bits(128, 16, 1024);
     for (int i = 0; i < n; ++i) {
@@ -379,15 +390,14 @@ __global__ void __launch_bounds__(kTcThreads) shrink_tc_kernel(LoraRows rows, Sh
   __syncthreads();  // the MMAs are done, and nothing of the stages is read or written any more
 
   float* red = reinterpret_cast<float*>(sm);
-  if (warp >= 2) {
+  if (warp < 4) {
     tc_fence_after();
-    const int quad = warp & 3;  // the lanes of tensor memory that this warp may read
-    float* mine = red + (quad * 32 + lane) * L::kPitch;
+    float* mine = red + threadIdx.x * L::kPitch;  // warp w may read lanes 32 w .. of tensor memory
 #pragma unroll
     for (int c = 0; c < RP; c += 16) {
       uint32_t v[16];
       if (n > 0) {
-        tmem_ld_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, v);
+        tmem_ld_x16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
         tmem_wait_ld_r16(v);
       } else {
 #pragma unroll
@@ -401,28 +411,29 @@ __global__ void __launch_bounds__(kTcThreads) shrink_tc_kernel(LoraRows rows, Sh
   }
   __syncthreads();
   if (cs > 1) cluster_sync();
-  if (warp == 1) {
+  if (warp == 4) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
+  } else {
+    finish_rows<BF16, RT, 128, L::kPitch>(p, tile, red, cs, crank, threadIdx.x);
   }
-  if (warp >= 2) finish_rows<BF16, RT, 128, L::kPitch>(p, tile, red, cs, crank, threadIdx.x - 64);
   __syncwarp();
   if (cs > 1) cluster_sync();  // no CTA ends while another reads its sums
 }
 
 // ------------------------------------------------------------------ launches
-// Shares of a contraction of `len`: as many as give `want` CTAs, each of at
-// least four steps of 64.
-int shares(int64_t tiles, int len, int64_t want) {
+// Shares of a contraction of `len`: as many as make up to `room` CTAs, each of
+// at least four steps of 64.
+int shares(int64_t tiles, int len, int64_t room) {
   int cs = 1;
-  while (cs < 8 && tiles * cs < want && (len + 63) / 64 >= 8 * cs) cs *= 2;
+  while (cs < 8 && tiles * cs * 2 <= room && (len + 63) / 64 >= 8 * cs) cs *= 2;
   return cs;
 }
 
 template <bool BF16, int RT, bool BOTH>
 cudaError_t shrink_few(const LoraRows& rows, const ShrinkParams* p, int rank, int sms, cudaStream_t s) {
   const int64_t tiles = most_tiles(rows.m, rows.adapters, 16);
-  const int cs = shares(tiles * (BOTH ? 2 : 1), BOTH ? std::max(p[0].len, p[1].len) : p[0].len, 4 * sms);
+  const int cs = shares(tiles * (BOTH ? 2 : 1), BOTH ? std::max(p[0].len, p[1].len) : p[0].len, 8 * sms);
   size_t smem = FewSmem<RT>::kRed;
   if (BOTH) smem = std::max<size_t>(smem, FewSmem<RT>::kStage * FewSmem<RT>::kStages);
   auto kernel = shrink_few_kernel<BF16, RT, BOTH>;
@@ -432,53 +443,32 @@ cudaError_t shrink_few(const LoraRows& rows, const ShrinkParams* p, int rank, in
 }
 
 template <bool BF16, int RT, bool BOTH>
-cudaError_t shrink_many(const LoraRows& rows, const ShrinkParams* p, const TcMaps& maps, int sms, cudaStream_t s) {
+cudaError_t shrink_many(const LoraRows& rows, const ShrinkParams* p, int rank, int sms, cudaStream_t s) {
   const int64_t tiles = most_tiles(rows.m, rows.adapters, 128);
-  const int cs = shares(tiles * (BOTH ? 2 : 1), BOTH ? std::max(p[0].len, p[1].len) : p[0].len, 2 * sms);
+  // two CTAs per SM, but for SMs that a cluster's placement leaves free
+  const int cs =
+      shares(tiles * (BOTH ? 2 : 1), BOTH ? std::max(p[0].len, p[1].len) : p[0].len, 2 * sms * 7 / 8);
   auto kernel = shrink_tc_kernel<BF16, RT, BOTH>;
   if (const cudaError_t e = allow_smem(kernel, ShrinkTc<RT>::kBytes); e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs), BOTH ? 2 : 1), dim3(kTcThreads),
-                    ShrinkTc<RT>::kBytes, cs, s, rows, p[0], p[BOTH ? 1 : 0], maps, cs, device_error_word());
-}
-
-// The maps of x (gathered rows) and of the weights of one contraction.
-wqmm_status shrink_maps(const LoraRows& rows, const ShrinkParams& p, int rank, bool rank_major, bool bf16,
-                        CUtensorMap* x, CUtensorMap* w) {
-  const uint64_t xe[2] = {static_cast<uint64_t>(p.len), static_cast<uint64_t>(rows.m)};
-  const uint64_t xs[1] = {static_cast<uint64_t>(p.x.ld) * 2};
-  const uint32_t xb[2] = {64, 1};
-  wqmm_status st = tensor_map16(x, p.x.p, bf16, 2, xe, xs, xb, 128);
-  if (st) return st;
-  const int rp = lora_padded_rank(rank);
-  const uint64_t in = rank_major ? rank : p.len, out = rank_major ? p.len : rank;
-  const uint64_t we[3] = {in, out, static_cast<uint64_t>(rows.adapters)};
-  const uint64_t ws[2] = {in * 2, in * out * 2};
-  const uint32_t cols = rank_major ? std::min(rp, 64) : 64;
-  const uint32_t wb[3] = {cols, static_cast<uint32_t>(rank_major ? 64 : rp), 1};
-  return tensor_map16(w, p.w, bf16, 3, we, ws, wb, static_cast<int>(cols) * 2);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs), BOTH ? 2 : 1), dim3(kShrinkThreads),
+                    ShrinkTc<RT>::kBytes, cs, s, rows, p[0], p[BOTH ? 1 : 0], rank, cs, device_error_word());
 }
 
 }  // namespace
 
 int lora_padded_rank(int rank) { return 16 * padded_sixteenths(rank); }
 
-wqmm_status launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
+cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
                                cudaStream_t s) {
-  TcMaps maps;
-  const bool few = few_rows(rows);
-  if (!few)
-    for (int i = 0; i < count; ++i)
-      if (const wqmm_status st = shrink_maps(rows, p[i], rank, i == 1, bf16, &maps.x[i], &maps.w[i])) return st;
-  const cudaError_t e = with_rank(rank, [&](auto rt) {
+  return with_rank(rank, [&](auto rt) {
     constexpr int RT = decltype(rt)::value;
     auto pick = [&](auto t, auto both) {
       constexpr bool T = decltype(t)::value, B = decltype(both)::value;
-      return few ? shrink_few<T, RT, B>(rows, p, rank, sms, s) : shrink_many<T, RT, B>(rows, p, maps, sms, s);
+      return few_rows(rows) ? shrink_few<T, RT, B>(rows, p, rank, sms, s) : shrink_many<T, RT, B>(rows, p, rank, sms, s);
     };
     auto by_count = [&](auto t) { return count == 2 ? pick(t, std::true_type()) : pick(t, std::false_type()); };
     return bf16 ? by_count(std::true_type()) : by_count(std::false_type());
   });
-  return e == cudaSuccess ? WQMM_SUCCESS : cuda_fail(e, "adapter contraction launch");
 }
 
 }  // namespace wqmm

@@ -1,32 +1,21 @@
 // lora_tc.cuh -- what the adapters' tcgen05 kernels (lora_shrink.cu,
-// lora_outer.cu) share: gathered tensor copies, shared-memory operand
-// descriptors for both majors, and tensor map shapes.
+// lora_outer.cu) share: shared-memory operands of both majors and the copies
+// that fill them.
+//
+// The rows of a tile lie anywhere in x (the order of the adapters), so they are
+// copied by four warps with 16-byte asynchronous copies, 128 to 256
+// neighbouring bytes of a row by the lanes next to each other; a gathering
+// tensor copy (four rows of 128 bytes each) moved 7 bytes per clock and SM
+// where 23 are wanted.  A warp that has waited for its copies of a stage makes
+// them visible to the MMA (fence.proxy.async) and arrives on the stage's
+// barrier.
 #pragma once
 #include "lora_common.cuh"
 
 namespace wqmm {
 namespace {
 
-constexpr int kTcThreads = 192;  // copy warp, MMA warp, four warps for the rest
-
-// Four rows of a tensor map whose box is one row of 64 columns: row i of the
-// four at dst + 128 i (128-byte swizzle).  A row outside the tensor reads as zeros.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t col, int4 r) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
-      "%5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(col), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1,
-                                            int32_t c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-      "[%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
+constexpr int kCopyThreads = 128;  // warps 0 to 3
 
 // D[tmem] (+)= A[smem] * B[smem]^T, kind::f16.
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -50,29 +39,40 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint64_t bits) { retu
 
 constexpr uint32_t kAMn = 1u << 15, kBMn = 1u << 16;  // instruction descriptor: operand is MN-major
 
-// A rank-wide operand (RP columns, 64 rows along the contraction, MN-major):
-// bytes of a row of one block, of the whole, and its descriptor.
+// Byte of 16-byte chunk c of row r where rows of ROW bytes are swizzled.
+template <int ROW>
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+  return r * ROW + ((c ^ (ROW == 128 ? r & 7 : ROW == 64 ? (r >> 1) & 3 : (r >> 2) & 1)) * 16);
+}
+
+// A rank-wide operand: 64 rows along the contraction (MN-major) of RP columns,
+// in blocks of up to 64 columns.
 template <int RT>
 struct RankRows {
   static constexpr int RP = RT * 16;
-  static constexpr int kCols = RP < 64 ? RP : 64;  // columns of one block (one tensor copy)
-  static constexpr int kBlocks = RP / kCols;
+  static constexpr int kCols = RP < 64 ? RP : 64;  // of one block
   static constexpr int kRow = kCols * 2;
   static constexpr int kBlock = 64 * kRow;
-  static constexpr int kBytes = kBlocks * kBlock;
-  static constexpr uint64_t kBits = operand_bits(kRow, kBlocks > 1 ? kBlock : 16, 8 * kRow);
+  static constexpr int kBytes = RP / kCols * kBlock;
+  static constexpr uint64_t kBits = operand_bits(kRow, RP > kCols ? kBlock : 16, 8 * kRow);
   static constexpr uint32_t kStep = 16 * kRow;  // bytes from one MMA's sixteen rows to the next
-};
-
-// Both contractions' tensor maps.
-struct TcMaps {
-  CUtensorMap x[2];  // gathered rows: box 64 columns x 1 row, 128-byte swizzle
-  CUtensorMap w[2];
+  // byte of columns 8 c .. 8 c + 7 of row r
+  static __device__ __forceinline__ uint32_t at(int r, int c) {
+    constexpr int C = kCols / 8;
+    return c / C * kBlock + swizzled<kRow>(r, c % C);
+  }
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err,
                                           uint32_t code) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err, code));
+}
+
+// What a copying warp does once its copies of a stage have landed.
+__device__ __forceinline__ void hand_over(uint64_t* full) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(full);
 }
 
 }  // namespace
