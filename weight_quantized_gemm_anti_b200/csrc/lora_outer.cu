@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
                                                                  uint32_t* err) {
   using L = OuterTc<RT>;
   using R = RankRows<RT>;
-  constexpr int S = L::kStages, RP = L::RP, LAG = S - 2;  // LAG: steps under way behind the newest
+  constexpr int S = L::kStages, RP = L::RP;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t full[S], empty[S], sums_full[2], sums_empty[2], top_ready[2], done;
   __shared__ uint32_t tmem_sh;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   if (warp < 4 && first < items) {
     const Item o = item_at(first);
     find(o, 0);
-    for (; early < LAG && early < o.n; ++early) {
+    for (; early < S && early < o.n; ++early) {
       copy_x(o, early);
       find(o, early + 1);
     }
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   if (warp < 4) {
     // ---------------------------------------------------------------- copies
     // (after a wait that gave up these warps still go through the items, for the barriers among them)
-    int g = 0, k = 0, handed = 0;  // steps begun, items, steps handed over
+    int g = 0, k = 0;  // steps, items
     bool live = true;
     for (int it = first; it < items; it += stride, ++k) {
       const Item o = item_at(it);
@@ -232,19 +232,10 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
           store_low(st);
           load_low(o, i + 1, below);
         }
-        cp_async_commit();
-        if (handed <= g - LAG) {
-          cp_async_wait_group<LAG>();
-          hand_over(&full[handed++ % S]);
-        }
-      }
-      // the item's last steps are handed over now: its sums do not wait for the next item's copies
-      if (live) {
-        cp_async_wait_group<0>();
-        for (; handed < g; ++handed) hand_over(&full[handed % S]);
+        hand_over(&full[st]);
       }
     }
-    cp_async_wait_group<0>();
+    copies_landed();
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMAs
     constexpr uint32_t kIdesc = idesc_make(1u, BF16 ? 1u : 0u, 128, RP) | kAMn | kBMn;
@@ -259,11 +250,10 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
       const uint32_t d = tmem + buf * RP;
       for (int i = 0; i < o.n; ++i, ++g) {
         const int st = g % S;
-        if (!warp_wait(&full[st], (g / S) & 1, abort, err, kDevTimeoutMma)) {
+        if (!stage_wait(&full[st], (g / S) & 1, abort, err)) {
           live = false;
           break;
         }
-        tc_fence_after();
         const uint32_t xs = base + st * L::kStage, ls = xs + L::kX;
         if (elect_one()) {
 #pragma unroll

@@ -269,7 +269,7 @@ __device__ __forceinline__ void shrink_copies(const LoraRows& rows, const Shrink
                                               int s0, int n, uint32_t base, uint64_t* full, uint64_t* empty,
                                               volatile int* abort, uint32_t* err) {
   using L = ShrinkTc<RT>;
-  constexpr int S = L::kStages, LAG = S - 2;  // steps under way behind the newest
+  constexpr int S = L::kStages;
   const int tid = threadIdx.x;
   const uint16_t* w = p.w + static_cast<int64_t>(tile.group) * rank * p.len;
   // 16-byte chunk c of rows tid / 8 + 16 i of x (and of a k-major W)
@@ -281,8 +281,7 @@ __device__ __forceinline__ void shrink_copies(const LoraRows& rows, const Shrink
     x[i] = v >= 0 ? p.x.p + v * p.x.ld : nullptr;
   }
   const uint32_t to = swizzled<128>(r, c);
-  int i = 0;
-  for (; i < n; ++i) {
+  for (int i = 0; i < n; ++i) {
     const int st = i % S;
     if (i >= S && !warp_wait(&empty[st], ((i / S) & 1) ^ 1, abort, err, kDevTimeoutProducer)) break;
     const uint32_t xs = base + st * L::kStage, ws = xs + L::kX;
@@ -304,14 +303,9 @@ __device__ __forceinline__ void shrink_copies(const LoraRows& rows, const Shrink
         cp16(ws + RankRows<RT>::at(wr, wc), has ? w + static_cast<int64_t>(kk) * rank + wc * 8 : w, has);
       }
     }
-    cp_async_commit();
-    if (i >= LAG) {
-      cp_async_wait_group<LAG>();
-      hand_over(&full[(i - LAG) % S]);
-    }
+    hand_over(&full[st]);
   }
-  cp_async_wait_group<0>();
-  for (int j = i > LAG ? i - LAG : 0; j < i; ++j) hand_over(&full[j % S]);
+  copies_landed();
 }
 
 template <bool BF16, int RT, bool BOTH>
@@ -366,8 +360,7 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_tc_kernel(LoraRows rows
     constexpr uint64_t kKBits = operand_bits(128, 16, 1024);
     for (int i = 0; i < n; ++i) {
       const int st = i % S;
-      if (!warp_wait(&full[st], (i / S) & 1, abort, err, kDevTimeoutMma)) break;
-      tc_fence_after();
+      if (!stage_wait(&full[st], (i / S) & 1, abort, err)) break;
       const uint32_t xs = base + st * L::kStage, ws = xs + L::kX;
       if (elect_one()) {
 #pragma unroll

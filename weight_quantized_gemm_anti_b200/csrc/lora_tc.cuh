@@ -6,9 +6,8 @@
 // copied by four warps with 16-byte asynchronous copies, 128 to 256
 // neighbouring bytes of a row by the lanes next to each other; a gathering
 // tensor copy (four rows of 128 bytes each) moved 7 bytes per clock and SM
-// where 23 are wanted.  A warp that has waited for its copies of a stage makes
-// them visible to the MMA (fence.proxy.async) and arrives on the stage's
-// barrier.
+// where 23 are wanted.  A stage's barrier counts the
+// copies as they land.
 #pragma once
 #include "lora_common.cuh"
 
@@ -68,11 +67,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err, code));
 }
 
-// What a copying warp does once its copies of a stage have landed.
+// A copying warp hands a stage over without waiting for its copies: the barrier
+// counts them when they land.
 __device__ __forceinline__ void hand_over(uint64_t* full) {
-  fence_proxy_async_smem();
+  cp_async_mbar_arrive(full);
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(full);
+}
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// The MMA warp's wait for a stage.  What threads have written to shared memory
+// becomes visible to the tensor core by the fence; the waiting side makes it,
+// since a copying thread's would wait for all its copies under way.
+__device__ __forceinline__ bool stage_wait(uint64_t* full, uint32_t parity, volatile int* abort, uint32_t* err) {
+  if (!warp_wait(full, parity, abort, err, kDevTimeoutMma)) return false;
+  fence_proxy_async_smem();
+  tc_fence_after();
+  return true;
 }
 
 }  // namespace
