@@ -90,19 +90,12 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool has) {
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool has) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(has ? 4 : 0) : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
+// The two halves of a cluster barrier.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // ------------------------------------------------------------------ tiles of rows
 // Tile t of the sorted rows when every group of rows is cut into tiles of `bm`:
@@ -110,39 +103,37 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 // `bare`, the rows of none behind them.  The offsets are clamped to [0, m], so
 // that no value of theirs leads out of the tensors.  Called by whole warps.
 struct Tile {
-  int group;
-  int64_t p0, p1;
+  int group, p0, p1;
 };
-__device__ __forceinline__ int64_t offset_at(const LoraRows& r, int g) {
-  if (g > r.adapters) return r.m;
-  const int64_t v = r.offsets[g];
-  return v < 0 ? 0 : (v > r.m ? r.m : v);
+__device__ __forceinline__ int offset_at(const LoraRows& r, int g) {
+  const int m = static_cast<int>(r.m);
+  return g > r.adapters ? m : min(max(r.offsets[g], 0), m);
 }
-__device__ __forceinline__ bool find_tile(const LoraRows& r, int bare, int bm, int64_t t, Tile& out) {
+__device__ __forceinline__ bool find_tile(const LoraRows& r, int bare, int bm, int t, Tile& out) {
   const int lane = threadIdx.x & 31;
   const int groups = r.adapters + bare;
   for (int g0 = 0; g0 < groups; g0 += 32) {
     const int g = g0 + lane;
-    int64_t lo = 0, hi = 0;
+    int lo = 0, hi = 0;
     if (g < groups) {
       lo = offset_at(r, g);
       hi = offset_at(r, g + 1);
     }
-    const int64_t n = hi > lo ? (hi - lo + bm - 1) / bm : 0;
-    int64_t upto = n;
+    const int n = hi > lo ? (hi - lo - 1) / bm + 1 : 0;
+    int upto = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
+      const int v = __shfl_up_sync(0xffffffffu, upto, d);
       if (lane >= d) upto += v;
     }
-    const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+    const int all = __shfl_sync(0xffffffffu, upto, 31);
     if (t < all) {
       const int at = __popc(__ballot_sync(0xffffffffu, upto <= t));
-      const int64_t first = __shfl_sync(0xffffffffu, upto - n, at);
+      const int first = __shfl_sync(0xffffffffu, upto - n, at);
       out.group = g0 + at;
       out.p1 = __shfl_sync(0xffffffffu, hi, at);
       out.p0 = __shfl_sync(0xffffffffu, lo, at) + (t - first) * bm;
-      if (out.p1 > out.p0 + bm) out.p1 = out.p0 + bm;
+      if (out.p1 - out.p0 > bm) out.p1 = out.p0 + bm;
       return true;
     }
     t -= all;
@@ -150,10 +141,10 @@ __device__ __forceinline__ bool find_tile(const LoraRows& r, int bare, int bm, i
   return false;
 }
 // Row of a sorted place, -1 behind the tile (or where the order names no row).
-__device__ __forceinline__ int64_t row_at(const LoraRows& r, int64_t p, int64_t p1) {
+__device__ __forceinline__ int row_at(const LoraRows& r, int p, int p1) {
   if (p >= p1) return -1;
-  const int64_t v = r.source[p];
-  return v >= 0 && v < r.m ? v : -1;
+  const int v = r.source[p];
+  return v < r.m ? v : -1;
 }
 // Most tiles that m rows in `groups` groups can make.
 int64_t most_tiles(int64_t m, int groups, int bm) {

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
 
   // this thread's two rows: their places in y and out
   const int wrow = WM == 1 ? 0 : warp * 16;
-  int64_t row[2];
+  int row[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) row[i] = row_at(rows, tile.p0 + wrow + g + 8 * i, tile.p1);
   uint4 y[GROUPS][2];
@@ -114,10 +114,10 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
   uint32_t a[2][RT][4];  // hi, lo
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int64_t place = tile.p0 + wrow + g + 8 * i;
+    const int place = tile.p0 + wrow + g + 8 * i;
     const bool has = with && place < tile.p1;
     if (!BF16 && has) factor[i] = p.low.factor[place];
-    const uint32_t* low = reinterpret_cast<const uint32_t*>(p.low.low + (has ? place * (2 * RP) : 0));
+    const uint32_t* low = reinterpret_cast<const uint32_t*>(p.low.low + (has ? static_cast<int64_t>(place) * (2 * RP) : 0));
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll

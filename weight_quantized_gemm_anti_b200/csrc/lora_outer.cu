@@ -9,8 +9,8 @@ namespace {
 // row of low lie along the contraction as they are in memory.  low's two
 // 16-bit numbers are two MMAs into the same sums.
 //
-// Roles: four warps copy the rows of x (in the order of their adapters) and of
-// low, one issues the MMAs, four write the sums.  Rows behind the adapter's last
+// Roles: four warps copy the rows of x (in the order of their adapters), four
+// those of low, one issues the MMAs, four write the sums.  Rows behind the adapter's last
 // are zeros in both operands.  float16 rows of low have a power of two each;
 // on their way to shared memory they are brought to the largest of the CTA's rows.
 //
@@ -18,7 +18,7 @@ namespace {
 // shares one, each CTA a part of the rows, and the parts meet in shared memory
 // in the order of the CTAs; with many a CTA goes through several, the copies of
 // the next under way while one is written (its sums are in tensor memory twice).
-constexpr int kOuterThreads = kCopyThreads + 128 + 32;
+constexpr int kOuterThreads = 2 * kCopyThreads + 128 + 32;
 
 template <int RT>
 struct OuterTc {
@@ -26,12 +26,11 @@ struct OuterTc {
   static constexpr int kX = 2 * 64 * 128;             // two blocks of 64 columns
   static constexpr int kLow = RankRows<RT>::kBytes;   // one of the two numbers
   static constexpr int kStage = kX + 2 * kLow;
-  static constexpr int kStages = RT == 1 ? 5 : RT == 2 ? 4 : RT == 4 ? 3 : 4;  // two CTAs per SM; one of rank 128
-  static constexpr int kPerSm = RT == 8 ? 1 : 2;
-  static constexpr int kBytes = kStage * kStages + 1024;
+  static constexpr int kStages = RT == 1 ? 4 : RT == 2 ? 3 : RT == 4 ? 5 : 3;  // two CTAs per SM up to rank 32
+  static constexpr int kPerSm = RT < 4 ? 2 : 1;
+  static constexpr int kPitch = RP + 4;  // of the sums, floats: rows a bank group apart
+  static constexpr int kBytes = kStage * kStages + 128 * kPitch * 4 + 1024;
   static constexpr uint32_t kCols = 2 * RP < 32 ? 32 : 2 * RP;
-  static constexpr int kPitch = RP + 1;  // of the sums, floats
-  static_assert(128 * kPitch * 4 <= kStage * kStages, "the sums reuse the stages");
 };
 
 // Two neighbours of the gradient: columns c (and c + 1 in the rank-row form), rank rows r (and r + 1 otherwise).
@@ -61,7 +60,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
 
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 4);
+      mbar_init(&full[i], 8);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -77,8 +76,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
 
   // an item's adapter, columns and steps; its rows are [r0, r1), this CTA's those from `begin` in n steps of 64
   struct Item {
-    int which, c0, adapter, n;
-    int64_t begin, r1;
+    int which, c0, adapter, n, begin, r1;
   };
   auto item_at = [&](int it) {
     Item o;
@@ -86,12 +84,12 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     const int ct = it % tiles;
     o.which = ct < tiles0 ? 0 : 1;
     o.c0 = (ct < tiles0 ? ct : ct - tiles0) * 128;
-    const int64_t r0 = offset_at(rows, o.adapter);
+    const int r0 = offset_at(rows, o.adapter);
     o.r1 = max(offset_at(rows, o.adapter + 1), r0);
-    const int64_t steps = (o.r1 - r0 + 63) / 64;
-    const int64_t s0 = steps * crank / cs;
+    const int steps = o.r1 > r0 ? (o.r1 - r0 - 1) / 64 + 1 : 0;
+    const int s0 = static_cast<int>(static_cast<int64_t>(steps) * crank / cs);
     o.begin = r0 + s0 * 64;
-    o.n = static_cast<int>(steps * (crank + 1) / cs - s0);
+    o.n = static_cast<int>(static_cast<int64_t>(steps) * (crank + 1) / cs) - s0;
     return o;
   };
 
@@ -101,7 +99,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   const uint32_t xto = (xc >> 3) * 8192 + swizzled<128>(xr, xc & 7);
   int number = -1;
   auto find = [&](const Item& o, int i) {
-    const int64_t place = o.begin + i * 64 + 2 * (warp & 3) + (lane & 1) + 8 * ((lane & 15) >> 1);
+    const int place = o.begin + i * 64 + 2 * (warp & 3) + (lane & 1) + 8 * ((lane & 15) >> 1);
     number = i < o.n && place < o.r1 ? rows.source[place] : -1;
   };
   auto copy_x = [&](const Item& o, int st) {
@@ -119,14 +117,14 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   // low: 16-byte chunk at % (4 RT) of row at / (4 RT), both numbers of a row side by side
   constexpr int kLowChunks = 2 * RT;  // per thread
   auto low_from = [&](const Item& o, int i, int j, bool& has) {
-    const int at = tid + j * kCopyThreads, r = at / (4 * RT), c = at % (4 * RT);
-    const int64_t place = o.begin + i * 64 + r;
+    const int at = (tid & 127) + j * kCopyThreads, r = at / (4 * RT), c = at % (4 * RT);
+    const int place = o.begin + i * 64 + r;
     has = i < o.n && place < o.r1;
     const uint16_t* low = (o.which == 0 ? p0 : p1).low.low;
-    return has ? low + place * (2 * RP) + c * 8 : low;
+    return has ? low + static_cast<int64_t>(place) * (2 * RP) + c * 8 : low;
   };
   auto low_to = [&](int st, int j) {
-    const int at = tid + j * kCopyThreads, r = at / (4 * RT), c = at % (4 * RT);
+    const int at = (tid & 127) + j * kCopyThreads, r = at / (4 * RT), c = at % (4 * RT);
     return st * L::kStage + L::kX + c / (2 * RT) * L::kLow + R::at(r, c % (2 * RT));
   };
   auto copy_low = [&](const Item& o, int i, int st) {  // bfloat16
@@ -146,7 +144,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
       const uint16_t* from = low_from(o, i, j, has);
       held[j] = has ? *reinterpret_cast<const uint4*>(from) : make_uint4(0, 0, 0, 0);
       held_by[j] =
-          has ? (o.which == 0 ? p0 : p1).low.factor[o.begin + i * 64 + (tid + j * kCopyThreads) / (4 * RT)] * below : 0.f;
+          has ? (o.which == 0 ? p0 : p1).low.factor[o.begin + i * 64 + ((tid & 127) + j * kCopyThreads) / (4 * RT)] * below : 0.f;
     }
   };
   auto store_low = [&](int st) {
@@ -174,6 +172,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
       find(o, early + 1);
     }
   }
+  if (cs > 1) cluster_arrive();
   pdl_wait();
   pdl_trigger();
   // tensor memory is taken now: the launch before this one may have held it all
@@ -184,12 +183,36 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (cs > 1) cluster_wait();  // the others have begun
   const uint32_t tmem = tmem_sh;
 
   if (warp < 4) {
-    // ---------------------------------------------------------------- copies
+    // ---------------------------------------------------------------- rows of x
+    int g = 0;
+    bool live = true;
+    for (int it = first; it < items && live; it += stride) {
+      const Item o = item_at(it);
+      const int had = it == first ? early : 0;
+      if (had == 0) find(o, 0);
+      for (int i = 0; i < o.n; ++i, ++g) {
+        const int st = g % S;
+        if (g >= S && !warp_wait(&empty[st], ((g / S) & 1) ^ 1, abort, err, kDevTimeoutProducer)) {
+          live = false;
+          break;
+        }
+        if (i >= had) {
+          copy_x(o, st);
+          find(o, i + 1);
+        }
+        hand_over(&full[st]);
+      }
+    }
+    copies_landed();
+  } else if (warp >= 9) {
+    // ---------------------------------------------------------------- rows of low
     // (after a wait that gave up these warps still go through the items, for the barriers among them)
-    int g = 0, k = 0;  // steps, items
+    const int t = tid & 127;
+    int g = 0, k = 0;
     bool live = true;
     for (int it = first; it < items; it += stride, ++k) {
       const Item o = item_at(it);
@@ -197,35 +220,29 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
       if constexpr (!BF16) {
         // the largest power of two of this CTA's rows
         const float* factor = (o.which == 0 ? p0 : p1).low.factor + o.begin;
-        const int n = static_cast<int>(min(static_cast<int64_t>(o.n) * 64, o.r1 - o.begin));
+        const int n = min(o.n * 64, o.r1 - o.begin);
         float top = 0.f;
-        for (int r = tid; r < n; r += kCopyThreads) top = fmaxf(top, factor[r]);
+        for (int r = t; r < n; r += kCopyThreads) top = fmaxf(top, factor[r]);
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
         named_bar_sync(1, kCopyThreads);  // the last item's maxima are read
-        if (lane == 0) tops[warp] = top;
+        if (lane == 0) tops[warp & 3] = top;
         named_bar_sync(1, kCopyThreads);
         top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         if (!(top > 0.f)) top = 1.f;  // no rows
         below = 1.f / top;            // of a power of two: exact
         // the maximum of two items ago has been read when its sums have
         live = live && (k < 2 || warp_wait(&sums_empty[k & 1], ((k / 2) & 1) ^ 1, abort, err, kDevTimeoutDequant));
-        if (live && tid == 0) {
+        if (live && t == 0) {
           top_sh[k & 1] = top;
           mbar_arrive(&top_ready[k & 1]);
         }
         load_low(o, 0, below);
       }
-      const int had = it == first ? early : 0;
-      if (had == 0) find(o, 0);
       for (int i = 0; i < o.n; ++i, ++g) {
         const int st = g % S;
         live = live && (g < S || warp_wait(&empty[st], ((g / S) & 1) ^ 1, abort, err, kDevTimeoutProducer));
         if (!live) continue;
-        if (i >= had) {
-          copy_x(o, st);
-          find(o, i + 1);
-        }
         if constexpr (BF16) {
           copy_low(o, i, st);
         } else {
@@ -291,7 +308,11 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
       }
       tc_fence_after();
       uint16_t* out = p.out + static_cast<int64_t>(o.adapter) * rank * p.len;
-      float* red = reinterpret_cast<float*>(sm) + col * L::kPitch;  // a cluster's only item: the stages are free
+      // a cluster's CTA c writes the columns from c * 128 / cs: the others' sums of them go to its shared
+      // memory, [CTA][column][kPitch]
+      const int own = 128 / cs;
+      uint32_t sums = smem_u32(sm + L::kStage * S) + (crank * own + col % own) * L::kPitch * 4;
+      if (cs > 1) sums = mapa_shared(sums, col / own);
 #pragma unroll
       for (int c = 0; c < RP; c += 16) {
         uint32_t v[16];
@@ -304,7 +325,9 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
         }
         if (cs > 1) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) red[c + i] = __uint_as_float(v[i]) * top;
+          for (int i = 0; i < 16; i += 4)
+            st_cluster_f32x4(sums + (c + i) * 4, __uint_as_float(v[i]) * top, __uint_as_float(v[i + 1]) * top,
+                             __uint_as_float(v[i + 2]) * top, __uint_as_float(v[i + 3]) * top);
         } else if (p.rank_rows) {
           // a rank row's neighbours are in the neighbour lanes: pairs of two rows at a time
 #pragma unroll
@@ -338,43 +361,29 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     tmem_dealloc(tmem, L::kCols);
   }
   if (cs > 1) {
-    cluster_sync();
-    const Item o = item_at(first);
-    const OuterParams& p = o.which == 0 ? p0 : p1;
-    uint16_t* out = p.out + static_cast<int64_t>(o.adapter) * rank * p.len;
-    const float* red = reinterpret_cast<const float*>(sm);
-    // two neighbours of the result per thread; the CTAs of the cluster share the columns
-    const int cols = 128 / cs, cb = crank * cols;
-    for (int at = threadIdx.x; at < cols * rank / 2; at += kOuterThreads) {
-      int c[2], r[2];
-      if (p.rank_rows) {
-        const int half = cols / 2;
-        c[0] = cb + (at % half) * 2;
-        c[1] = c[0] + 1;
-        r[0] = r[1] = at / half;
-      } else {
-        const int half = rank / 2;
-        c[0] = c[1] = cb + at / half;
-        r[0] = (at % half) * 2;
-        r[1] = r[0] + 1;
-      }
-      if (o.c0 + c[0] >= p.len) continue;
-      float f[8][2], v[2] = {0.f, 0.f};
+    cluster_arrive();
+    cluster_wait();
+    const int ct = first % tiles, own = 128 / cs;
+    const OuterParams& p = ct < tiles0 ? p0 : p1;
+    const int c0 = (ct < tiles0 ? ct : ct - tiles0) * 128 + crank * own;
+    uint16_t* out = p.out + static_cast<int64_t>(first / tiles) * rank * p.len;
+    const float* sums = reinterpret_cast<const float*>(sm + L::kStage * S);
+    // two neighbours of the result per thread
+    for (int at = tid; at < own * rank / 2; at += kOuterThreads) {
+      const int half = (p.rank_rows ? own : rank) / 2;
+      const int c = p.rank_rows ? at % half * 2 : at / half, r = p.rank_rows ? at / half : at % half * 2;
+      if (c0 + c >= p.len) continue;
+      const int step = p.rank_rows ? L::kPitch : 1;
+      float a = 0.f, b = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < cs)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            f[j][i] = ld_cluster_f32(mapa_shared(smem_u32(red + c[i] * L::kPitch + r[i]), j));
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < cs)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) v[i] += f[j][i];
-      put_pair<BF16>(out, p, rank, o.c0 + c[0], r[0], v[0], v[1]);
+        if (j < cs) {
+          const float* s = sums + (j * own + c) * L::kPitch + r;
+          a += s[0];
+          b += s[step];
+        }
+      put_pair<BF16>(out, p, rank, c0 + c, r, a, b);
     }
-    __syncwarp();
-    cluster_sync();  // no CTA ends while another reads its sums
   }
 }
 

@@ -5,36 +5,40 @@ namespace wqmm {
 namespace {
 
 // ------------------------------------------------------------------ the shares' sums
-// A tile of rows is shared by the CTAs of a cluster, each with a part of the
-// contraction and its sums [BM][PITCH] in shared memory at `red`.  The CTAs deal
-// the rows among themselves and add the parts in the order of the CTAs, so the
-// result does not depend on timing.  Then scale, the row's power of two
-// (float16) and the two 16-bit numbers.  Called by kThreads threads, tid 0 ...
+// A tile of BM rows is shared by the CTAs of a cluster, each with a part of the
+// contraction.  CTA c finishes the BM / cs rows from c * BM / cs: the others write
+// their sums of these into its shared memory, [CTA][row][PITCH], and it adds them
+// in the order of the CTAs, so the result does not depend on timing.  Then scale,
+// the row's power of two (float16) and the two 16-bit numbers.  Called by
+// kThreads threads, tid 0 ...
+template <int BM, int PITCH>
+__device__ __forceinline__ uint32_t sums_of_row(const float* sums, int r, int cs, int crank) {
+  const int own = BM / cs;
+  const uint32_t at = smem_u32(sums + (crank * own + r % own) * PITCH);
+  return cs > 1 ? mapa_shared(at, r / own) : at;
+}
+
 template <bool BF16, int RT, int BM, int PITCH>
-__device__ __forceinline__ void finish_rows(const ShrinkParams& p, const Tile& tile, const float* red, int cs,
+__device__ __forceinline__ void finish_rows(const ShrinkParams& p, const Tile& tile, const float* sums, int cs,
                                             int crank, int tid) {
   constexpr int RP = RT * 16;
   constexpr int LANES = RP / 4, PER = kThreads / LANES;  // four values of a row per lane
-  const int sub = tid % LANES;
+  const int sub = tid % LANES, own = BM / cs;
   const float scale = p.scale ? p.scale[tile.group] : 1.f;
-  for (int r0 = crank * PER; r0 < BM; r0 += cs * PER) {
+  for (int r0 = 0; r0 < own; r0 += PER) {
     const int r = r0 + tid / LANES;
-    const int64_t place = tile.p0 + r;
-    const bool live = r < BM && place < tile.p1;
+    const int place = tile.p0 + crank * own + r;
+    const bool live = r < own && place < tile.p1;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (live) {
-      const uint32_t at = smem_u32(red + r * PITCH + sub * 4);
-      float4 f[8];  // all CTAs' parts in flight at once
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (c < cs) f[c] = ld_cluster_f32x4(cs > 1 ? mapa_shared(at, c) : at);
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         if (c < cs) {
-          v[0] += f[c].x;
-          v[1] += f[c].y;
-          v[2] += f[c].z;
-          v[3] += f[c].w;
+          const float4 f = *reinterpret_cast<const float4*>(sums + (c * own + r) * PITCH + sub * 4);
+          v[0] += f.x;
+          v[1] += f.y;
+          v[2] += f.z;
+          v[3] += f.w;
         }
     }
 #pragma unroll
@@ -71,7 +75,7 @@ __device__ __forceinline__ void finish_rows(const ShrinkParams& p, const Tile& t
         const float ha = Half<BF16>::get(hi[i] & 0xffff), hb = Half<BF16>::get(hi[i] >> 16);
         lo[i] = Half<BF16>::put2(isfinite(ha) ? a - ha : 0.f, isfinite(hb) ? b - hb : 0.f);
       }
-      uint16_t* o = p.out.low + place * (2 * RP) + sub * 4;
+      uint16_t* o = p.out.low + static_cast<int64_t>(place) * (2 * RP) + sub * 4;
       *reinterpret_cast<uint2*>(o) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(o + RP) = make_uint2(lo[0], lo[1]);
     }
@@ -96,7 +100,7 @@ __device__ __forceinline__ void few_rows_sum(const LoraRows& rows, const ShrinkP
   const uint16_t* x[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int64_t r = row_at(rows, tile.p0 + g + 8 * i, tile.p1);
+    const int r = row_at(rows, tile.p0 + g + 8 * i, tile.p1);
     x[i] = r >= 0 ? p.x.p + r * p.x.ld + q * 8 : nullptr;
   }
   const uint16_t* w = p.w + (static_cast<int64_t>(tile.group) * rank + g) * p.len + q * 8;
@@ -151,7 +155,7 @@ __device__ __forceinline__ void few_rows_staged_sum(const LoraRows& rows, const 
   const uint16_t* w = p.w + static_cast<int64_t>(tile.group) * rank * p.len;
   // this thread's part of x: 16-byte chunk tid % 8 of row tid / 8
   const int xc = tid & 7, xr = tid / 8;
-  const int64_t row = row_at(rows, tile.p0 + xr, tile.p1);
+  const int row = row_at(rows, tile.p0 + xr, tile.p1);
   const uint16_t* x = p.x.p + (row >= 0 ? row * p.x.ld : 0);
   auto load = [&](int step, int stage) {
     const uint32_t xs = base + stage * L::kStage, ws = xs + L::kX;
@@ -211,9 +215,11 @@ __device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const Shrink
   else
     few_rows_staged_sum<BF16, RT>(rows, p, rank, tile, s0, s1, sm, acc);
 
-  float* red = reinterpret_cast<float*>(sm);
+  // the warps' sums, then the CTA's, then the cluster's
+  float* sums = reinterpret_cast<float*>(sm + (KM ? 0 : FewSmem<RT>::kStage * FewSmem<RT>::kStages));
+  float* part = sums + 16 * RP;
   {
-    float* mine = red + (1 + warp) * 16 * RP;
+    float* mine = part + warp * 16 * RP;
     const int g = lane >> 2, q = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -222,14 +228,21 @@ __device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const Shrink
     }
   }
   __syncthreads();
-  for (int at = tid; at < 16 * RP; at += kThreads)
-    red[at] = (red[16 * RP + at] + red[32 * RP + at]) + (red[48 * RP + at] + red[64 * RP + at]);
-  if (cs > 1)
-    cluster_sync();
-  else
+  if (cs > 1) cluster_wait();  // the others have begun
+  for (int at = tid * 4; at < 16 * RP; at += kThreads * 4) {
+    const float4 a = *reinterpret_cast<const float4*>(part + at), b = *reinterpret_cast<const float4*>(part + 16 * RP + at),
+                 c = *reinterpret_cast<const float4*>(part + 32 * RP + at),
+                 d = *reinterpret_cast<const float4*>(part + 48 * RP + at);
+    st_cluster_f32x4(sums_of_row<16, RP>(sums, at / RP, cs, crank) + at % RP * 4, (a.x + b.x) + (c.x + d.x),
+                     (a.y + b.y) + (c.y + d.y), (a.z + b.z) + (c.z + d.z), (a.w + b.w) + (c.w + d.w));
+  }
+  if (cs > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
     __syncthreads();
-  finish_rows<BF16, RT, 16, RP>(p, tile, red, cs, crank, tid);
-  if (cs > 1) cluster_sync();  // no CTA ends while another reads its sums
+  }
+  finish_rows<BF16, RT, 16, RP>(p, tile, sums, cs, crank, tid);
 }
 
 template <bool BF16, int RT, bool BOTH>
@@ -240,6 +253,7 @@ __global__ void __launch_bounds__(kThreads) shrink_few_kernel(LoraRows rows, Shr
   pdl_trigger();
   Tile tile;
   if (!find_tile(rows, 0, 16, blockIdx.x / cs, tile)) return;  // the same for the whole cluster
+  if (cs > 1) cluster_arrive();
   if (!BOTH || blockIdx.y == 0)
     few_rows_tile<BF16, RT, true>(rows, p0, rank, cs, tile, sm);
   else
@@ -256,30 +270,24 @@ struct ShrinkTc {
   static constexpr int RP = RT * 16;
   static constexpr int kX = 128 * 128, kW = RP * 128;
   static constexpr int kStage = kX + kW;
-  static constexpr int kStages = RT == 1 ? 6 : RT == 2 ? 5 : RT == 4 ? 4 : 3;  // two CTAs per SM
+  static constexpr int kStages = RT == 1 ? 5 : RT == 2 ? 4 : RT == 4 ? 3 : 4;  // two CTAs per SM; one of rank 128
+  static constexpr int kPerSm = RT == 8 ? 1 : 2;
   static constexpr int kPitch = RP + 4;  // of the sums, floats: rows a bank group apart
-  static constexpr int kBytes = kStage * kStages + 1024;
+  static constexpr int kBytes = kStage * kStages + 128 * kPitch * 4 + 1024;
   static constexpr uint32_t kCols = RP < 32 ? 32 : RP;
-  static_assert(128 * kPitch * 4 <= kStage * kStages, "the sums reuse the stages");
 };
 constexpr int kShrinkThreads = kCopyThreads + 32;
 
 template <bool BF16, int RT, bool KM>
-__device__ __forceinline__ void shrink_copies(const LoraRows& rows, const ShrinkParams& p, int rank, const Tile& tile,
-                                              int s0, int n, uint32_t base, uint64_t* full, uint64_t* empty,
-                                              volatile int* abort, uint32_t* err) {
+__device__ __forceinline__ void shrink_copies(const ShrinkParams& p, int rank, const Tile& tile,
+                                              const uint16_t* const (&x)[8], int s0, int n, uint32_t base,
+                                              uint64_t* full, uint64_t* empty, volatile int* abort, uint32_t* err) {
   using L = ShrinkTc<RT>;
   constexpr int S = L::kStages;
   const int tid = threadIdx.x;
   const uint16_t* w = p.w + static_cast<int64_t>(tile.group) * rank * p.len;
   // 16-byte chunk c of rows tid / 8 + 16 i of x (and of a k-major W)
   const int c = tid & 7, r = tid >> 3;
-  const uint16_t* x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t v = row_at(rows, tile.p0 + r + 16 * i, tile.p1);
-    x[i] = v >= 0 ? p.x.p + v * p.x.ld : nullptr;
-  }
   const uint32_t to = swizzled<128>(r, c);
   for (int i = 0; i < n; ++i) {
     const int st = i % S;
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_tc_kernel(LoraRows rows
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const bool km = !BOTH || blockIdx.y == 0;
   const ShrinkParams& p = km ? p0 : p1;
   if (threadIdx.x == 0) {
@@ -332,16 +340,26 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_tc_kernel(LoraRows rows
     fence_barrier_init();
   }
   pdl_wait();
-  pdl_trigger();
   Tile tile;
   if (!find_tile(rows, 0, 128, blockIdx.x / cs, tile)) return;  // the same for the whole cluster
+  if (cs > 1) cluster_arrive();
   if (warp == 4) {
     tmem_alloc(&tmem_sh, L::kCols);
     tmem_relinquish();
   }
+  // rows tid / 8 + 16 i of the tile
+  const uint16_t* x[8];
+  if (warp < 4) {
+    int v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = row_at(rows, tile.p0 + (threadIdx.x >> 3) + 16 * i, tile.p1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[i] >= 0 ? p.x.p + v[i] * p.x.ld : nullptr;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_trigger();
   const uint32_t tmem = tmem_sh;
   volatile int* abort = &abort_sh;
   const int crank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -352,9 +370,9 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_tc_kernel(LoraRows rows
 
   if (warp < 4) {
     if (km)
-      shrink_copies<BF16, RT, true>(rows, p, rank, tile, s0, n, base, full, empty, abort, err);
+      shrink_copies<BF16, RT, true>(p, rank, tile, x, s0, n, base, full, empty, abort, err);
     else
-      shrink_copies<BF16, RT, false>(rows, p, rank, tile, s0, n, base, full, empty, abort, err);
+      shrink_copies<BF16, RT, false>(p, rank, tile, x, s0, n, base, full, empty, abort, err);
   } else {
     constexpr uint32_t kIdesc = idesc_make(1u, BF16 ? 1u : 0u, 128, RP);
     constexpr uint64_t kKBits = operand_bits(128, 16, 1024);
@@ -380,12 +398,13 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_tc_kernel(LoraRows rows
     volatile int no_abort = 0;
     warp_wait(&done, 0, &no_abort, err, kDevTimeoutDrain);
   }
-  __syncthreads();  // the MMAs are done, and nothing of the stages is read or written any more
+  __syncthreads();  // the MMAs are done
+  if (cs > 1) cluster_wait();  // the others have begun
 
-  float* red = reinterpret_cast<float*>(sm);
+  float* sums = reinterpret_cast<float*>(sm + L::kStage * S);
   if (warp < 4) {
     tc_fence_after();
-    float* mine = red + threadIdx.x * L::kPitch;  // warp w may read lanes 32 w .. of tensor memory
+    const uint32_t mine = sums_of_row<128, L::kPitch>(sums, threadIdx.x, cs, crank);  // warp w reads lanes 32 w ..
 #pragma unroll
     for (int c = 0; c < RP; c += 16) {
       uint32_t v[16];
@@ -398,37 +417,45 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_tc_kernel(LoraRows rows
       }
 #pragma unroll
       for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<uint4*>(mine + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        st_cluster_f32x4(mine + (c + i) * 4, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
+                         __uint_as_float(v[i + 3]));
     }
     tc_fence_before();
   }
   __syncthreads();
-  if (cs > 1) cluster_sync();
+  if (cs > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == 4) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
   } else {
-    finish_rows<BF16, RT, 128, L::kPitch>(p, tile, red, cs, crank, threadIdx.x);
+    finish_rows<BF16, RT, 128, L::kPitch>(p, tile, sums, cs, crank, threadIdx.x);
   }
-  __syncwarp();
-  if (cs > 1) cluster_sync();  // no CTA ends while another reads its sums
 }
 
 // ------------------------------------------------------------------ launches
-// Shares of a contraction of `len`: as many as make up to `room` CTAs, each of
-// at least four steps of 64.
-int shares(int64_t tiles, int len, int64_t room) {
+// Shares of the contractions, at most 8: such that the longer one's shares are
+// as long as an even deal of all steps of 64 to `room` CTAs makes them, or
+// longer, and have at least four steps.
+int shares(int64_t tiles, const ShrinkParams* p, int count, int64_t room) {
+  int64_t all = 0, longest = 0;
+  for (int i = 0; i < count; ++i) {
+    const int64_t steps = (p[i].len + 63) / 64;
+    all += tiles * steps;
+    longest = std::max(longest, steps);
+  }
   int cs = 1;
-  while (cs < 8 && tiles * cs * 2 <= room && (len + 63) / 64 >= 8 * cs) cs *= 2;
+  while (cs < 8 && 2 * cs * all <= longest * room && longest >= 8 * cs) cs *= 2;
   return cs;
 }
 
 template <bool BF16, int RT, bool BOTH>
 cudaError_t shrink_few(const LoraRows& rows, const ShrinkParams* p, int rank, int sms, cudaStream_t s) {
   const int64_t tiles = most_tiles(rows.m, rows.adapters, 16);
-  const int cs = shares(tiles * (BOTH ? 2 : 1), BOTH ? std::max(p[0].len, p[1].len) : p[0].len, 8 * sms);
-  size_t smem = FewSmem<RT>::kRed;
-  if (BOTH) smem = std::max<size_t>(smem, FewSmem<RT>::kStage * FewSmem<RT>::kStages);
+  const int cs = shares(tiles, p, BOTH ? 2 : 1, 8 * sms);
+  const size_t smem = FewSmem<RT>::kRed + (BOTH ? FewSmem<RT>::kStage * FewSmem<RT>::kStages : 0);
   auto kernel = shrink_few_kernel<BF16, RT, BOTH>;
   if (const cudaError_t e = allow_smem(kernel, smem); e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs), BOTH ? 2 : 1), dim3(kThreads), smem, cs, s, rows,
@@ -438,9 +465,8 @@ cudaError_t shrink_few(const LoraRows& rows, const ShrinkParams* p, int rank, in
 template <bool BF16, int RT, bool BOTH>
 cudaError_t shrink_many(const LoraRows& rows, const ShrinkParams* p, int rank, int sms, cudaStream_t s) {
   const int64_t tiles = most_tiles(rows.m, rows.adapters, 128);
-  // two CTAs per SM, but for SMs that a cluster's placement leaves free
-  const int cs =
-      shares(tiles * (BOTH ? 2 : 1), BOTH ? std::max(p[0].len, p[1].len) : p[0].len, 2 * sms * 7 / 8);
+  // as many CTAs as run at once, but for SMs that a cluster's placement leaves free
+  const int cs = shares(tiles, p, BOTH ? 2 : 1, ShrinkTc<RT>::kPerSm * sms * 7 / 8);
   auto kernel = shrink_tc_kernel<BF16, RT, BOTH>;
   if (const cudaError_t e = allow_smem(kernel, ShrinkTc<RT>::kBytes); e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs), BOTH ? 2 : 1), dim3(kShrinkThreads),
