@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
       const uint32_t ws = base + buf * L::kBuf;
       constexpr int C = RP / 8;
 #pragma unroll
-      for (int i = 0; i < 128 * C / kThreads; ++i) {
+      for (int i = 0; i < (128 * C + kThreads - 1) / kThreads; ++i) {
         const int at = tid + i * kThreads, col = at / C, c = at % C;
         const bool has = c0 + col < c_end && c * 8 < rank;
         // column (q, j, e) of its group of 32 goes to row (j, q, e)
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
 #pragma unroll
       for (int i = 0; i < WR; ++i) {
         const int at = tid + i * kThreads, r = at / 4, col = c0 + (at % 4) * 32;
-        const bool has = r < rank && col < c_end;
+        const bool has = r < rank && r < RP && col < c_end;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           wr[i][j] = has ? *reinterpret_cast<const uint4*>(w + static_cast<int64_t>(r) * p.len + col + j * 8)
@@ -94,16 +94,16 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
   int row[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) row[i] = row_at(rows, tile.p0 + wrow + g + 8 * i, tile.p1);
-  uint4 y[GROUPS][2];
+  uint4 y[GROUPS][2], next[GROUPS][2];
   auto fetch_y = [&](int c0) {
 #pragma unroll
     for (int s = 0; s < GROUPS; ++s)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int col = c0 + (WM == 1 ? warp : s) * 32 + q * 8;
-        y[s][i] = make_uint4(0, 0, 0, 0);
+        next[s][i] = make_uint4(0, 0, 0, 0);
         if (p.y.p && row[i] >= 0 && col < c_end)
-          y[s][i] = *reinterpret_cast<const uint4*>(p.y.p + row[i] * p.y.ld + col);
+          next[s][i] = *reinterpret_cast<const uint4*>(p.y.p + row[i] * p.y.ld + col);
       }
   };
   fetch_y(c_begin);
@@ -129,7 +129,11 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
 
   int buf = 0;
   for (int c0 = c_begin; c0 < c_end; c0 += 128, buf ^= 1) {
-    if (c0 > c_begin) fetch_y(c0);
+#pragma unroll
+    for (int s = 0; s < GROUPS; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) y[s][i] = next[s][i];
+    if (c0 + 128 < c_end) fetch_y(c0 + 128);
     if (with) {
       put(buf);
       __syncthreads();  // this chunk's weights are there, and the other buffer is read no more
@@ -188,10 +192,11 @@ template <bool BF16, int RT, bool KM, int WM>
 cudaError_t expand_as(const LoraRows& rows, const ExpandParams& p, int rank, int sms, cudaStream_t s) {
   constexpr int BM = WM * 16;
   const int64_t tiles = most_tiles(rows.m, rows.adapters + p.bare, BM);
-  // columns per CTA: up to 1024, fewer where there would be under eight CTAs per SM
+  // columns per CTA: up to 1024, fewer where there would be under two CTAs per SM (4096 x 4096, rank 16: two
+  // CTAs 28.5 us with the contraction before, eight 30.1), or eight of the short-lived ones of few rows
   const int all = (p.len + 127) / 128;
   int chunks = 8;
-  while (chunks > 1 && tiles * ((all + chunks - 1) / chunks) < 8 * sms) chunks /= 2;
+  while (chunks > 1 && tiles * ((all + chunks - 1) / chunks) < (WM == 1 ? 8 : 2) * sms) chunks /= 2;
   auto kernel = expand_kernel<BF16, RT, KM, WM>;
   const size_t smem = ExpandSmem<RT, KM>::kBytes;
   if (const cudaError_t e = allow_smem(kernel, smem); e != cudaSuccess) return e;

@@ -19,12 +19,11 @@ __device__ __forceinline__ uint32_t sums_of_row(const float* sums, int r, int cs
 }
 
 template <bool BF16, int RT, int BM, int PITCH>
-__device__ __forceinline__ void finish_rows(const ShrinkParams& p, const Tile& tile, const float* sums, int cs,
-                                            int crank, int tid) {
+__device__ __forceinline__ void finish_rows(const ShrinkParams& p, const Tile& tile, float scale, const float* sums,
+                                            int cs, int crank, int tid) {
   constexpr int RP = RT * 16;
   constexpr int LANES = RP / 4, PER = kThreads / LANES;  // four values of a row per lane
   const int sub = tid % LANES, own = BM / cs;
-  const float scale = p.scale ? p.scale[tile.group] : 1.f;
   for (int r0 = 0; r0 < own; r0 += PER) {
     const int r = r0 + tid / LANES;
     const int place = tile.p0 + crank * own + r;
@@ -95,7 +94,7 @@ template <bool BF16, int RT>
 __device__ __forceinline__ void few_rows_sum(const LoraRows& rows, const ShrinkParams& p, int rank, const Tile& tile,
                                              int k0, int k1, float (&acc)[RT * 2][4]) {
   constexpr int NT = RT * 2;
-  constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;  // 32s in flight: 16 to 18 loads
+  constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;  // 32s in flight: 10 to 18 loads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   const uint16_t* x[2];
 #pragma unroll
@@ -205,6 +204,7 @@ __device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const Shrink
   const int steps = (p.len + 63) / 64;
   const int s0 = static_cast<int>(static_cast<int64_t>(steps) * crank / cs);
   const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (crank + 1) / cs);
+  const float scale = p.scale ? p.scale[tile.group] : 1.f;
   float acc[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -242,7 +242,7 @@ __device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const Shrink
   } else {
     __syncthreads();
   }
-  finish_rows<BF16, RT, 16, RP>(p, tile, sums, cs, crank, tid);
+  finish_rows<BF16, RT, 16, RP>(p, tile, scale, sums, cs, crank, tid);
 }
 
 template <bool BF16, int RT, bool BOTH>
@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_tc_kernel(LoraRows rows
   const int s0 = static_cast<int>(static_cast<int64_t>(steps) * crank / cs);
   const int n = static_cast<int>(static_cast<int64_t>(steps) * (crank + 1) / cs) - s0;  // this CTA's steps
   const uint32_t base = smem_u32(sm);
+  const float scale = p.scale ? p.scale[tile.group] : 1.f;
 
   if (warp < 4) {
     if (km)
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(kShrinkThreads) shrink_tc_kernel(LoraRows rows
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
   } else {
-    finish_rows<BF16, RT, 128, L::kPitch>(p, tile, sums, cs, crank, threadIdx.x);
+    finish_rows<BF16, RT, 128, L::kPitch>(p, tile, scale, sums, cs, crank, threadIdx.x);
   }
 }
 
