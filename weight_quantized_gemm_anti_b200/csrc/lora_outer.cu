@@ -20,16 +20,19 @@ namespace {
 // the next under way while one is written (its sums are in tensor memory twice).
 constexpr int kOuterThreads = 2 * kCopyThreads + 128 + 32;
 
-template <int RT>
+template <int RT, bool SHARED>  // SHARED: a cluster shares an item
 struct OuterTc {
   static constexpr int RP = RT * 16;
   static constexpr int kX = 2 * 64 * 128;             // two blocks of 64 columns
   static constexpr int kLow = RankRows<RT>::kBytes;   // one of the two numbers
   static constexpr int kStage = kX + 2 * kLow;
-  static constexpr int kStages = RT == 1 ? 4 : RT == 2 ? 3 : RT == 4 ? 5 : 3;  // two CTAs per SM up to rank 32
-  static constexpr int kPerSm = RT < 4 ? 2 : 1;
-  static constexpr int kPitch = RP + 4;  // of the sums, floats: rows a bank group apart
-  static constexpr int kBytes = kStage * kStages + 128 * kPitch * 4 + 1024;
+  static constexpr int kPitch = RP + 4;  // of the shares' sums, floats: rows a bank group apart
+  static constexpr int kSums = SHARED ? 128 * kPitch * 4 : 0;
+  // what two CTAs per SM leave room for, or one of the largest ranks
+  static constexpr int kPerSm = RT == 8 || (RT == 4 && SHARED) ? 1 : 2;
+  static constexpr int kStages = SHARED ? (RT == 1 ? 4 : RT == 2 ? 3 : RT == 4 ? 5 : 3)
+                                        : (RT == 1 ? 5 : RT == 2 ? 4 : RT == 4 ? 3 : 4);
+  static constexpr int kBytes = kStage * kStages + kSums + 1024;
   static constexpr uint32_t kCols = 2 * RP < 32 ? 32 : 2 * RP;
 };
 
@@ -40,11 +43,11 @@ __device__ __forceinline__ void put_pair(uint16_t* out, const OuterParams& p, in
   *reinterpret_cast<uint32_t*>(out + to) = Half<BF16>::put2(a, b);
 }
 
-template <bool BF16, int RT>
+template <bool BF16, int RT, bool SHARED>
 __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, OuterParams p0, OuterParams p1,
-                                                                 int rank, int cs, int tiles0, int tiles, int items,
+                                                                 int rank, int shares, int tiles0, int tiles, int items,
                                                                  uint32_t* err) {
-  using L = OuterTc<RT>;
+  using L = OuterTc<RT, SHARED>;
   using R = RankRows<RT>;
   constexpr int S = L::kStages, RP = L::RP;
   extern __shared__ uint8_t raw[];
@@ -55,7 +58,8 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int crank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int cs = SHARED ? shares : 1;
+  const int crank = SHARED ? static_cast<int>(cluster_ctarank()) : 0;
   const int first = blockIdx.x / cs, stride = gridDim.x / cs;
 
   if (tid == 0) {
@@ -137,20 +141,20 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   };
   uint4 held[BF16 ? 1 : kLowChunks];  // float16: the next step's low, and its rows' powers of two
   float held_by[BF16 ? 1 : kLowChunks];
-  auto load_low = [&](const Item& o, int i, float below) {
+  auto load_low = [&](const Item& o, int i) {
 #pragma unroll
     for (int j = 0; j < (BF16 ? 0 : kLowChunks); ++j) {
       bool has;
       const uint16_t* from = low_from(o, i, j, has);
       held[j] = has ? *reinterpret_cast<const uint4*>(from) : make_uint4(0, 0, 0, 0);
       held_by[j] =
-          has ? (o.which == 0 ? p0 : p1).low.factor[o.begin + i * 64 + ((tid & 127) + j * kCopyThreads) / (4 * RT)] * below : 0.f;
+          has ? (o.which == 0 ? p0 : p1).low.factor[o.begin + i * 64 + ((tid & 127) + j * kCopyThreads) / (4 * RT)] : 0.f;
     }
   };
-  auto store_low = [&](int st) {
+  auto store_low = [&](int st, float below) {
 #pragma unroll
     for (int j = 0; j < (BF16 ? 0 : kLowChunks); ++j) {
-      const __half2 by = __float2half2_rn(held_by[j]);
+      const __half2 by = __float2half2_rn(held_by[j] * below);
       uint32_t w[4] = {held[j].x, held[j].y, held[j].z, held[j].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -172,7 +176,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
       find(o, early + 1);
     }
   }
-  if (cs > 1) cluster_arrive();
+  if (SHARED) cluster_arrive();
   pdl_wait();
   pdl_trigger();
   // tensor memory is taken now: the launch before this one may have held it all
@@ -183,7 +187,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (cs > 1) cluster_wait();  // the others have begun
+  if (SHARED) cluster_wait();  // the others have begun
   const uint32_t tmem = tmem_sh;
 
   if (warp < 4) {
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
           top_sh[k & 1] = top;
           mbar_arrive(&top_ready[k & 1]);
         }
-        load_low(o, 0, below);
+        load_low(o, 0);
       }
       for (int i = 0; i < o.n; ++i, ++g) {
         const int st = g % S;
@@ -246,8 +250,8 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
         if constexpr (BF16) {
           copy_low(o, i, st);
         } else {
-          store_low(st);
-          load_low(o, i + 1, below);
+          store_low(st, below);
+          load_low(o, i + 1);
         }
         hand_over(&full[st]);
       }
@@ -312,7 +316,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
       // memory, [CTA][column][kPitch]
       const int own = 128 / cs;
       uint32_t sums = smem_u32(sm + L::kStage * S) + (crank * own + col % own) * L::kPitch * 4;
-      if (cs > 1) sums = mapa_shared(sums, col / own);
+      if (SHARED) sums = mapa_shared(sums, col / own);
 #pragma unroll
       for (int c = 0; c < RP; c += 16) {
         uint32_t v[16];
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = 0;
         }
-        if (cs > 1) {
+        if (SHARED) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
             st_cluster_f32x4(sums + (c + i) * 4, __uint_as_float(v[i]) * top, __uint_as_float(v[i + 1]) * top,
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
   }
-  if (cs > 1) {
+  if constexpr (SHARED) {
     cluster_arrive();
     cluster_wait();
     const int ct = first % tiles, own = 128 / cs;
@@ -388,20 +392,28 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
 }
 
 // ------------------------------------------------------------------ launches
-template <bool BF16, int RT>
-cudaError_t outer_as(const LoraRows& rows, const OuterParams (&p)[2], int rank, int sms, cudaStream_t s) {
-  using L = OuterTc<RT>;
-  const int t0 = (p[0].len + 127) / 128, tiles = t0 + (p[1].len + 127) / 128;
+template <bool BF16, int RT, bool SHARED>
+cudaError_t outer_as(const LoraRows& rows, const OuterParams (&p)[2], int rank, int cs, int tiles0, int tiles, int sms,
+                     cudaStream_t s) {
+  using L = OuterTc<RT, SHARED>;
   const int items = tiles * rows.adapters;
-  const int room = L::kPerSm * sms;
-  // shares of an adapter's rows: as many as there is room for at once, each of 128 rows or more on average
-  int cs = 1;
-  while (cs < 8 && static_cast<int64_t>(items) * cs * 2 <= room && rows.m / rows.adapters >= 256 * cs) cs *= 2;
-  const int grid = cs > 1 ? items * cs : std::min(items, room);
-  auto kernel = outer_tc_kernel<BF16, RT>;
+  const int grid = SHARED ? items * cs : std::min(items, L::kPerSm * sms);
+  auto kernel = outer_tc_kernel<BF16, RT, SHARED>;
   if (const cudaError_t e = allow_smem(kernel, L::kBytes); e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kOuterThreads), L::kBytes, cs, s, rows, p[0], p[1],
-                    rank, cs, t0, tiles, items, device_error_word());
+                    rank, cs, tiles0, tiles, items, device_error_word());
+}
+
+template <bool BF16, int RT>
+cudaError_t outer_plan(const LoraRows& rows, const OuterParams (&p)[2], int rank, int sms, cudaStream_t s) {
+  const int t0 = (p[0].len + 127) / 128, tiles = t0 + (p[1].len + 127) / 128;
+  // shares of an adapter's rows: as many as there is room for at once, each of 128 rows or more on average
+  const int64_t room = static_cast<int64_t>(OuterTc<RT, true>::kPerSm) * sms;
+  int cs = 1;
+  while (cs < 8 && static_cast<int64_t>(tiles) * rows.adapters * cs * 2 <= room && rows.m / rows.adapters >= 256 * cs)
+    cs *= 2;
+  return cs > 1 ? outer_as<BF16, RT, true>(rows, p, rank, cs, t0, tiles, sms, s)
+                : outer_as<BF16, RT, false>(rows, p, rank, 1, t0, tiles, sms, s);
 }
 
 }  // namespace
@@ -410,7 +422,7 @@ cudaError_t launch_lora_outer(const LoraRows& rows, const OuterParams (&p)[2], i
                               cudaStream_t s) {
   return with_rank(rank, [&](auto rt) {
     constexpr int RT = decltype(rt)::value;
-    return bf16 ? outer_as<true, RT>(rows, p, rank, sms, s) : outer_as<false, RT>(rows, p, rank, sms, s);
+    return bf16 ? outer_plan<true, RT>(rows, p, rank, sms, s) : outer_plan<false, RT>(rows, p, rank, sms, s);
   });
 }
 
