@@ -15,12 +15,12 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-import struct
 import threading
 from typing import Optional, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libwqmm.so")
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "wqmm.h")
 
 # ---------------------------------------------------------------- constants (from include/wqmm.h)
@@ -51,12 +51,12 @@ class WqmmTensor(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_binding_module = None
 
-# phase 1 of the operators with a shared phase 2: name, descriptors, then integers (and more descriptors)
-_PLANNED = [("route_sort_get_workspace_size", 1, 1), ("route_dispatch_get_workspace_size", 3, 0),
-            ("route_combine_get_workspace_size", 5, 0), ("route_combine_grad_get_workspace_size", 6, 0),
-            ("lora_get_workspace_size", 8, 0), ("lora_grad_get_workspace_size", 11, 0)]
-_TENSORS_AFTER = {"route_sort_get_workspace_size": 3}
+# phase 1 of the routing and adapter operators: how many descriptors each takes
+_PLANNED = {"route_sort_get_workspace_size": 4, "route_dispatch_get_workspace_size": 3,
+            "route_combine_get_workspace_size": 5, "route_combine_grad_get_workspace_size": 6,
+            "lora_get_workspace_size": 8, "lora_grad_get_workspace_size": 11}
 
 
 def build(force: bool = False) -> str:
@@ -94,11 +94,10 @@ def lib():
             L.wqmm_version.restype = ctypes.c_char_p
             L.qmm_debug_set_raw_accumulator.argtypes = [P, P]
             L.wqmm_debug_set_flag_wait.argtypes = [P, ctypes.c_uint64, I32]
-            # the routing and adapter operators: every descriptor a pointer to the struct's bytes
-            for name, tensors, ints in _PLANNED:
-                getattr(L, name).argtypes = [P] * tensors + [I64] * ints + [P] * (_TENSORS_AFTER.get(name, 0)) + [
-                    U64P, EXP]
+            for name, tensors in _PLANNED.items():
+                getattr(L, name).argtypes = [T] * tensors + [U64P, EXP]
                 getattr(L, name).restype = I32
+            L.route_sort_get_workspace_size.argtypes = [T, I64, T, T, T, U64P, EXP]
             for name in ("route_run", "lora_run"):
                 getattr(L, name).argtypes = [P, ctypes.c_uint64, P, P]
                 getattr(L, name).restype = I32
@@ -339,28 +338,18 @@ def _workspace(nbytes: int, device):
     return ws, ws.data_ptr()
 
 
-# ---------------------------------------------------------------- both phases of an operator on torch tensors
-_DESC_STRUCT = struct.Struct("=Qii3q3qii")  # wqmm_tensor, byte for byte
-_torch_codes: dict = {}
-
-
-def _desc_bytes(t) -> Optional[bytes]:
-    """The descriptor of a torch tensor as the struct's bytes (cheaper to make than a WqmmTensor: a call at a
-    few tokens is bound by the host)."""
-    if t is None:
-        return None
-    code = _torch_codes.get(t.dtype)
-    if code is None:
-        code = _torch_codes[t.dtype] = _torch_dtype_code(t)
-    shape, stride = t.shape, t.stride()
-    nd = len(shape)
-    if nd == 2:
-        return _DESC_STRUCT.pack(t.data_ptr(), code, 2, shape[0], shape[1], 0, stride[0], stride[1], 0, 0, 0)
-    if nd == 1:
-        return _DESC_STRUCT.pack(t.data_ptr(), code, 1, shape[0], 0, 0, stride[0], 0, 0, 0, 0)
-    if nd == 3:
-        return _DESC_STRUCT.pack(t.data_ptr(), code, 3, *shape, *stride, 0, 0)
-    raise ValueError(f"a tensor of 1 to 3 dimensions is expected, got {nd}")
+# ---------------------------------------------------------------- the routing and adapter operators on torch tensors
+def binding():
+    """The compiled torch binding of routing and lora (csrc/binding.cpp).  Raises if it has not been built."""
+    global _binding_module
+    if _binding_module is None:
+        import torch  # noqa: F401  (its libraries are the binding's)
+        lib()
+        if not os.path.exists(BINDING_PATH):
+            raise ImportError(f"{BINDING_PATH} is missing; build it with weight_quantized_gemm_anti_b200.build()")
+        from . import _binding
+        _binding_module = _binding
+    return _binding_module
 
 
 def _same_device(*tensors) -> int:
@@ -378,46 +367,15 @@ def _same_device(*tensors) -> int:
     return dev
 
 
-def _placed(device: int, stream):
-    """The context in which an operator on `device` allocates and launches: its device current, and `stream`
-    (a torch.cuda.Stream, a raw handle or None) too, so that what the call allocates belongs to that stream.
-    None where nothing has to change."""
+def _on_stream(stream, device=None):
+    """The context in which an operator allocates and launches on `stream`, a torch.cuda.Stream or a raw handle of
+    `device` (None: the current one), so that what the call allocates belongs to that stream."""
     import torch
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        elif stream.device_index != device:
-            raise ValueError(f"the stream is on device {stream.device_index}, the tensors on {device}")
-        return torch.cuda.stream(stream)  # makes its device current too
-    return None if torch.cuda.current_device() == device else torch.cuda.device(device)
-
-
-def _raw_stream(device: int) -> int:
-    """Handle of the current stream of `device`, by the call that makes no stream object where torch has it."""
-    global _raw_stream
-    import torch
-    direct = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    _raw_stream = direct or (lambda d: torch.cuda.current_stream(d).cuda_stream)
-    return _raw_stream(device)
-
-
-def _both_phases(phase1, run, device: int, *args) -> None:
-    """Phase 1 on descriptor bytes, the workspace, and phase 2 on the current stream of `device`."""
-    ws, ex = ctypes.c_uint64(0), ctypes.c_void_p(None)
-    st = phase1(*args, ctypes.byref(ws), ctypes.byref(ex))
-    if st:
-        check(st)
-    size, space = ws.value, None
-    if size:
-        import torch
-        try:
-            space = torch.empty(size, dtype=torch.uint8, device=device)
-        except BaseException:
-            wqmm_executor_destroy(ex)
-            raise
-    st = run(space.data_ptr() if size else None, size, ex, _raw_stream(device))
-    if st:
-        check(st)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    elif device is not None and stream.device_index != device:
+        raise ValueError(f"the stream is on device {stream.device_index}, the tensors on {device}")
+    return torch.cuda.stream(stream)  # makes its device current too
 
 
 def weight_quant_matmul(x1, x2_desc: WqmmTensor, antiquant_scale, antiquant_offset=None, bias=None, x3=None,

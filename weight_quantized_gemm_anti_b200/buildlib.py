@@ -1,16 +1,19 @@
-"""Build libwqmm.so in-tree with nvcc for sm_100a (no JIT cache, no GPU needed)."""
+"""Build libwqmm.so in-tree with nvcc for sm_100a (no JIT cache, no GPU needed), and beside it the compiled torch
+binding of the routing and adapter operators, _binding.so."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libwqmm.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["api.cu", "kernels_aux.cu", "kernels_wqmm.cu", "kernels_smallm.cu", "kernels_qmm.cu", "noalloc.cu",
            "route.cu", "kernels_route.cu", "lora.cu", "lora_shrink.cu", "lora_expand.cu",
            "lora_outer.cu"]
@@ -32,7 +35,8 @@ def _newest_input() -> float:
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
+    newest = _newest_input()
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING)):
         return LIB
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -49,9 +53,30 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + ".tmp"
-    subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"], check=True)
+    subprocess.run([cc, *ARCH, "-shared", "-Xlinker", "-soname=libwqmm.so", "-o", tmp, *objs, "-Xcompiler", "-fPIC"], check=True)
     os.replace(tmp, LIB)
+    build_binding(verbose)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    """Compile csrc/binding.cpp against this interpreter's torch and libwqmm.so beside it."""
+    import torch
+    from torch.utils import cpp_extension
+    include = [*cpp_extension.include_paths(), os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+               sysconfig.get_paths()["include"]]
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    # by nvcc, which links the shared C++ runtime that torch's libraries use
+    cmd = [nvcc(), *ARCH, "-O2", "-std=c++17", "-shared", "-cudart", "none", "-Xcompiler", "-fPIC,-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f for d in include for f in ("-isystem", d)),
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", LIB, "-Xlinker", "-rpath=$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

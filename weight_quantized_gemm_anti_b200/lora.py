@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import torch
 
-from . import _both_phases, _desc_bytes, _placed, _same_device, lib, weight_quant_matmul
+from . import _on_stream, _same_device, binding, weight_quant_matmul
 from .routing import TokenOrder, sort_tokens
 
 
@@ -29,18 +29,10 @@ def lora_add(x1, lora_a, lora_b, order: TokenOrder, scale=None, y=None, out=None
     """out[r] = y[r] + scale[a] * (x1[r] @ lora_a[a].T) @ lora_b[a].T, a the adapter of row r; a row without adapter
     gets y, or zeros.  x1 (m, k) or (b, s, k); lora_a (adapters, rank, k); lora_b (adapters, n, rank); scale
     (adapters) float32; ``out`` may be ``y``."""
-    device = _same_device(x1, lora_a, lora_b, order.offsets, order.source, scale, y, out)
-    where = _placed(device, stream)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, _same_device(x1, lora_a, lora_b, order.offsets, order.source, scale, y, out)):
             return lora_add(x1, lora_a, lora_b, order, scale, y, out)
-    if out is None:
-        out = x1.new_empty((*x1.shape[:-1], lora_b.shape[1]))
-    L = lib()
-    _both_phases(L.lora_get_workspace_size, L.lora_run, device, _desc_bytes(x1), _desc_bytes(lora_a),
-                 _desc_bytes(lora_b), _desc_bytes(scale), _desc_bytes(order.offsets), _desc_bytes(order.source),
-                 _desc_bytes(y), _desc_bytes(out))
-    return out
+    return binding().lora_add(x1, lora_a, lora_b, scale, order.offsets, order.source, y, out)
 
 
 def lora_weight_quant_matmul(x1, x2_desc, antiquant_scale, lora_a, lora_b, order: TokenOrder, lora_scale=None,
@@ -50,9 +42,8 @@ def lora_weight_quant_matmul(x1, x2_desc, antiquant_scale, lora_a, lora_b, order
     out = x1 @ ((x2 + antiquant_offset) * antiquant_scale) + bias + x3 + the adapters' part.  The projection is
     rounded to the output type before the adapters' part is added, and the sum once more."""
     device = _same_device(x1, antiquant_scale, antiquant_offset, bias, x3, out)
-    where = _placed(device, stream)
-    if where is not None:
-        with where:
+    if stream is not None or device != torch.cuda.current_device():
+        with torch.cuda.device(device) if stream is None else _on_stream(stream, device):
             return lora_weight_quant_matmul(x1, x2_desc, antiquant_scale, lora_a, lora_b, order, lora_scale,
                                             antiquant_offset, bias, x3, antiquant_group_size, out)
     out = weight_quant_matmul(x1, x2_desc, antiquant_scale, antiquant_offset, bias, x3, antiquant_group_size, out)
@@ -64,23 +55,12 @@ def lora_grad(grad, x1, lora_a, lora_b, order: TokenOrder, scale=None, grad_x=No
     """The gradients of ``lora_add`` given ``grad`` of its result (y's is ``grad`` itself): (for x1, lora_a, lora_b).
     ``grad_x`` (m, k): what else x1's gradient has, the projection's own part, added in 32 bits before the one
     rounding; with ``in_place`` the sum goes into that tensor.  ``need_grad_x`` False: None in x1's place."""
-    device = _same_device(grad, x1, lora_a, lora_b, order.offsets, order.source, scale, grad_x)
-    where = _placed(device, stream)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, _same_device(grad, x1, lora_a, lora_b, order.offsets, order.source, scale, grad_x)):
             return lora_grad(grad, x1, lora_a, lora_b, order, scale, grad_x, need_grad_x, in_place)
     if grad_x is None and in_place:
         raise ValueError("in_place needs a grad_x to add to")
     if grad_x is not None and not need_grad_x:
         raise ValueError("a grad_x is given, but need_grad_x is False")
-    out = None
-    if need_grad_x:
-        out = grad_x if in_place else x1.new_empty(x1.shape)
-    grad_a = lora_a.new_empty(lora_a.shape)
-    grad_b = lora_b.new_empty(lora_b.shape)
-    L = lib()
-    _both_phases(L.lora_grad_get_workspace_size, L.lora_run, device, _desc_bytes(grad), _desc_bytes(x1),
-                 _desc_bytes(lora_a), _desc_bytes(lora_b), _desc_bytes(scale), _desc_bytes(order.offsets),
-                 _desc_bytes(order.source), _desc_bytes(grad_x), _desc_bytes(out), _desc_bytes(grad_a),
-                 _desc_bytes(grad_b))
-    return out, grad_a, grad_b
+    return binding().lora_grad(grad, x1, lora_a, lora_b, scale, order.offsets, order.source, grad_x, need_grad_x,
+                               in_place)

@@ -20,7 +20,7 @@ from typing import NamedTuple, Optional, Sequence
 
 import torch
 
-from . import _both_phases, _desc_bytes, _placed, _same_device, lib, weight_quant_matmul
+from . import _on_stream, _same_device, binding, weight_quant_matmul
 
 
 class TokenOrder(NamedTuple):
@@ -33,78 +33,40 @@ class TokenOrder(NamedTuple):
 def sort_tokens(expert_ids, num_experts: int, stream=None) -> TokenOrder:
     """The stable order of the slots by expert: expert_ids (T), (T, K) or (b, s, K), int32 or int64; an id outside
     [0, num_experts) belongs to no expert (a dropped slot, or an expert of another rank)."""
-    device = _same_device(expert_ids)
-    where = _placed(device, stream)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, _same_device(expert_ids)):
             return sort_tokens(expert_ids, num_experts)
-    if not expert_ids.is_contiguous():
-        raise ValueError("expert_ids must be contiguous")
-    offsets = expert_ids.new_empty(max(int(num_experts), 0) + 1, dtype=torch.int32)
-    source = expert_ids.new_empty(expert_ids.numel(), dtype=torch.int32)
-    position = torch.empty_like(expert_ids, dtype=torch.int32)
-    L = lib()
-    _both_phases(L.route_sort_get_workspace_size, L.route_run, device, _desc_bytes(expert_ids), int(num_experts),
-                 _desc_bytes(offsets), _desc_bytes(source), _desc_bytes(position))
-    return TokenOrder(offsets, source, position)
+    return TokenOrder(*binding().sort_tokens(expert_ids, num_experts))
 
 
 def dispatch_tokens(x, order: TokenOrder, out=None, stream=None):
     """out[position[t, j]] = x[t] for every slot of an expert; x (T, hidden) or (b, s, hidden).  ``out``: (rows,
     hidden) of x's dtype, one row per slot unless given; rows of no slot keep what they hold (in an ``out`` made
     here that is uninitialised memory, behind order.offsets[-1])."""
-    device = _same_device(x, order.position, out)
-    where = _placed(device, stream)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, _same_device(x, order.position, out)):
             return dispatch_tokens(x, order, out)
-    if out is None:
-        out = x.new_empty((order.position.numel(), x.shape[-1]))
-    L = lib()
-    _both_phases(L.route_dispatch_get_workspace_size, L.route_run, device, _desc_bytes(x),
-                 _desc_bytes(order.position), _desc_bytes(out))
-    return out
+    return binding().dispatch_tokens(x, order.position, out)
 
 
 def combine_tokens(x_sorted, order: TokenOrder, weights=None, x3=None, out=None, stream=None):
     """out[t] = x3[t] + sum_j weights[t, j] * x_sorted[position[t, j]], in 32 bits, rounded once.  ``weights``:
     shape of position, float16, bfloat16 or float32; None: all one, which is also the gradient of
     ``dispatch_tokens``.  ``out``: (T, hidden) unless x3 or ``out`` says (b, s, hidden)."""
-    device = _same_device(x_sorted, order.position, weights, x3, out)
-    where = _placed(device, stream)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, _same_device(x_sorted, order.position, weights, x3, out)):
             return combine_tokens(x_sorted, order, weights, x3, out)
-    if out is None:
-        if x3 is not None:
-            out = torch.empty_like(x3)
-        else:
-            p = order.position.shape
-            tokens = p if len(p) == 1 else p[:-1]
-            out = x_sorted.new_empty((*tokens, x_sorted.shape[-1]))
-    L = lib()
-    _both_phases(L.route_combine_get_workspace_size, L.route_run, device, _desc_bytes(x_sorted),
-                 _desc_bytes(order.position), _desc_bytes(weights), _desc_bytes(x3), _desc_bytes(out))
-    return out
+    return binding().combine_tokens(x_sorted, order.position, weights, x3, out)
 
 
 def combine_tokens_grad(grad, x_sorted, order: TokenOrder, weights, out=None, stream=None):
     """The gradient of ``combine_tokens`` for x_sorted and weights, given ``grad`` of its result:
     (grad_sorted, grad_weights).  Rows of no slot keep what ``out`` (grad_sorted's tensor, made here unless given)
     holds; grad_weights of a slot of no expert is 0."""
-    device = _same_device(grad, x_sorted, order.position, weights, out)
-    where = _placed(device, stream)
-    if where is not None:
-        with where:
+    if stream is not None:
+        with _on_stream(stream, _same_device(grad, x_sorted, order.position, weights, out)):
             return combine_tokens_grad(grad, x_sorted, order, weights, out)
-    if out is None:
-        out = torch.empty_like(x_sorted)
-    grad_weights = torch.empty_like(weights)
-    L = lib()
-    _both_phases(L.route_combine_grad_get_workspace_size, L.route_run, device, _desc_bytes(grad),
-                 _desc_bytes(x_sorted), _desc_bytes(order.position), _desc_bytes(weights), _desc_bytes(out),
-                 _desc_bytes(grad_weights))
-    return out, grad_weights
+    return binding().combine_tokens_grad(grad, x_sorted, order.position, weights, out)
 
 
 def expert_weight_quant_matmul(x_sorted, order: TokenOrder, x2_descs: Sequence, antiquant_scales: Sequence,
@@ -115,9 +77,8 @@ def expert_weight_quant_matmul(x_sorted, order: TokenOrder, x2_descs: Sequence, 
     has rows.  ``bounds``: order.offsets on the host (None: read here, which waits for the stream).  Rows behind
     the last expert keep what ``out`` holds."""
     device = _same_device(x_sorted, out)
-    where = _placed(device, stream)
-    if where is not None:
-        with where:
+    if stream is not None or device != torch.cuda.current_device():
+        with torch.cuda.device(device) if stream is None else _on_stream(stream, device):
             return expert_weight_quant_matmul(x_sorted, order, x2_descs, antiquant_scales, antiquant_offsets, biases,
                                               antiquant_group_size, out, bounds)
     if bounds is None:
