@@ -23,11 +23,12 @@ namespace {
 // slots 32 at a time, the lanes of one group ranked by lane.  Every count is a
 // whole number added in a fixed place, so the order is stable and the same in
 // every run.  Ids outside [0, groups) make one more group, behind the others.
-constexpr int kBatch = 4;
+constexpr int kBatch = 4;        // slots per lane
+constexpr int kSortCluster = 8;  // CTAs
 
 // The lanes whose group is this lane's (groups are below 2^bits): one vote per
-// bit.  At 4096 slots and 256 groups a sort takes 8.4 us with it, 11.9 us with
-// __match_any_sync.
+// bit.  4096 slots in 256 groups, sorted by one CTA, took 8.4 us with it and 11.9 us
+// with __match_any_sync.
 __device__ __forceinline__ uint32_t same_group(int e, int bits) {
   uint32_t same = 0xffffffffu;
   for (int b = 0; b < bits; ++b) {
@@ -41,6 +42,16 @@ template <typename IdT>
 __device__ __forceinline__ int group_of(const IdT* ids, int64_t i, int groups) {
   const IdT v = ids[i];
   return (v >= 0 && v < static_cast<IdT>(groups)) ? static_cast<int>(v) : groups;
+}
+
+// A cluster neighbour's copy of a shared variable.
+__device__ __forceinline__ int load_of_cta(const int* mine, int cta) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+  uint32_t there;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(cta));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(there) : "memory");
+  return v;
 }
 
 template <typename IdT>
@@ -59,15 +70,19 @@ __global__ void __launch_bounds__(256) sort_count_kernel(SortParams p) {
     p.hist[static_cast<int64_t>(blockIdx.x) * (p.groups + 1) + e] = count[e];
 }
 
-// Shared memory: next[warps][groups + 1], total[groups + 1], the scan's warp sums [32].
-template <typename IdT>
+// CLUSTER: the chunks' CTAs are one cluster and read each other's counts in
+// shared memory; otherwise the counts of all chunks are in hist, from the kernel
+// above (or there is one chunk).
+// Shared memory: next[warps][groups + 1], total[groups + 1], count[groups + 1], the scan's warp sums [32].
+template <typename IdT, bool CLUSTER>
 __global__ void __launch_bounds__(1024) sort_place_kernel(SortParams p) {
   extern __shared__ int sm[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int buckets = p.groups + 1;
   int* next = sm;
   int* total = sm + warps * buckets;
-  int* sums = total + buckets;
+  int* count = total + buckets;
+  int* sums = count + buckets;
   for (int i = threadIdx.x; i < warps * buckets; i += blockDim.x) next[i] = 0;
   pdl_wait();
   pdl_trigger();
@@ -104,11 +119,29 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortParams p) {
   }
   __syncthreads();
 
+  if constexpr (CLUSTER) {
+    for (int e = threadIdx.x; e < buckets; e += blockDim.x) {
+      int all = 0;
+      for (int w = 0; w < warps; ++w) all += next[w * buckets + e];
+      count[e] = all;
+    }
+    cluster_arrive();
+    cluster_wait();
+  }
   // per group: the runs' counts become first places within the chunk's slots of
   // the group, behind those of earlier chunks
   for (int e = threadIdx.x; e < buckets; e += blockDim.x) {
     int before = 0, all = 0;
-    if (p.chunks > 1) {
+    if constexpr (CLUSTER) {
+      int n[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) n[c] = c < p.chunks ? load_of_cta(count + e, c) : 0;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        all += n[c];
+        before += c < static_cast<int>(blockIdx.x) ? n[c] : 0;
+      }
+    } else if (p.chunks > 1) {
 #pragma unroll 8
       for (int c = 0; c < p.chunks; ++c) {
         const int n = p.hist[static_cast<int64_t>(c) * buckets + e];
@@ -123,6 +156,7 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortParams p) {
     }
     total[e] = p.chunks > 1 ? all : before;
   }
+  if constexpr (CLUSTER) cluster_arrive();  // this CTA has read the others' counts
   __syncthreads();
 
   // exclusive scan of total over the groups: consecutive ones per thread
@@ -173,6 +207,7 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(SortParams p) {
       __syncwarp();
     }
   }
+  if constexpr (CLUSTER) cluster_wait();  // the others have read this CTA's
 }
 
 // ------------------------------------------------------------------ vectors
@@ -473,39 +508,42 @@ cudaError_t dispatch_bytes(const DispatchParams& p, cudaStream_t s) {
   return p.tokens * (p.row_bytes / VB) >= 148 * 2048 * 4 ? dispatch_as<VB, 4>(p, s) : dispatch_as<VB, 1>(p, s);
 }
 
-size_t place_smem(int warps, int groups) { return (static_cast<size_t>(warps + 1) * (groups + 1) + 32) * 4; }
+size_t place_smem(int warps, int groups) { return (static_cast<size_t>(warps + 2) * (groups + 1) + 32) * 4; }
 
 template <typename IdT>
 cudaError_t sort_as(const SortParams& p, cudaStream_t s) {
-  int threads = 256;
-  if (p.chunks > 1) {
+  const bool cluster = p.chunks > 1 && p.chunks <= kSortCluster;
+  if (p.chunks > kSortCluster) {
     const cudaError_t e = launch_pdl(sort_count_kernel<IdT>, dim3(p.chunks), dim3(256),
                                      static_cast<size_t>(p.groups + 1) * 4, 1, s, p);
     if (e != cudaSuccess) return e;
-  } else {
-    threads = static_cast<int>(std::min<int64_t>(1024, std::max<int64_t>(64, (p.slots + 31) / 32 * 32)));
   }
+  // a batch per warp where the chunk and shared memory allow it
+  int threads = std::min(1024, std::max(64, (p.chunk / kBatch + 31) & ~31));
   while (place_smem(threads / 32, p.groups) > 200 * 1024) threads = (threads / 2 + 31) & ~31;
   const size_t smem = place_smem(threads / 32, p.groups);
-  if (const cudaError_t e = allow_smem(sort_place_kernel<IdT>, smem); e != cudaSuccess) return e;
-  return launch_pdl(sort_place_kernel<IdT>, dim3(p.chunks), dim3(threads), smem, 1, s, p);
+  auto kernel = cluster ? sort_place_kernel<IdT, true> : sort_place_kernel<IdT, false>;
+  if (const cudaError_t e = allow_smem(kernel, smem); e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(p.chunks), dim3(threads), smem, cluster ? p.chunks : 1, s, p);
 }
 
 }  // namespace
 
 uint64_t plan_sort(SortParams& p) {
-  // Up to 4096 slots one CTA sorts in one launch (7.5 us there; two launches take 6.1 us, but cost the host
-  // another 4); beyond, chunks of 1024 slots (65536: 15 us; chunks of 512: 26 us), larger ones where there
-  // would be more than 128, since every CTA reads all counts.
-  if (p.slots <= 4096) {
-    p.chunk = static_cast<int>(std::max<int64_t>(32, p.slots));
-    p.chunks = 1;
-    return 0;
-  }
-  const int64_t chunk = std::max<int64_t>(1024, ((p.slots + 127) / 128 + 255) / 256 * 256);
+  // Up to 1024 slots one CTA, up to 32768 a cluster of up to eight with 1024 or
+  // more each, in one launch (6162 slots: 5.0 us; with the counts in memory, two
+  // launches, 6.9 us; 32768: 9.4 and 9.9); beyond, chunks of 1024 (65536: 15 us;
+  // of 512: 26 us), larger ones where there would be more than 128, since every
+  // CTA reads all counts.
+  const int64_t slots = std::max<int64_t>(32, p.slots);
+  int64_t chunk = slots;
+  if (slots > 32768)
+    chunk = std::max<int64_t>(1024, ((slots + 127) / 128 + 255) / 256 * 256);
+  else if (slots > 1024)
+    chunk = std::max<int64_t>(1024, ((slots + kSortCluster - 1) / kSortCluster + 127) / 128 * 128);
   p.chunk = static_cast<int>(chunk);
-  p.chunks = static_cast<int>((p.slots + chunk - 1) / chunk);
-  return static_cast<uint64_t>(p.chunks) * (p.groups + 1) * 4;
+  p.chunks = static_cast<int>((slots + chunk - 1) / chunk);
+  return p.chunks > kSortCluster ? static_cast<uint64_t>(p.chunks) * (p.groups + 1) * 4 : 0;
 }
 
 cudaError_t launch_sort(const SortParams& p, cudaStream_t s) {

@@ -93,10 +93,6 @@ __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool has) {
 __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
-// The two halves of a cluster barrier.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
 // ------------------------------------------------------------------ tiles of rows
 // Tile t of the sorted rows when every group of rows is cut into tiles of `bm`:
 // its group and its rows [p0, p1).  The groups are the adapters and, with
