@@ -82,15 +82,15 @@ __device__ __forceinline__ void finish_rows(const ShrinkParams& p, const Tile& t
 }
 
 // ------------------------------------------------------------------ few rows
-// Tiles of 16 rows: the four warps split the contraction.
+// Tiles of 16 rows: the warps split the contraction, NW of them.
 
 // Few rows, k-major weights: nothing is shared between the warps, so the
 // matrix instruction's operands come straight from global memory.  A thread
 // loads 16 bytes of its rows and of its weight rows, eight neighbours of the
 // contraction; four threads' 32 make two steps of the instruction.  Which
 // element stands for which of a step's sixteen does not matter to the sum as
-// long as both operands agree.  Each warp takes every fourth 32.
-template <bool BF16, int RT>
+// long as both operands agree.  Each warp takes every NW-th 32.
+template <bool BF16, int RT, int NW>
 __device__ __forceinline__ void few_rows_sum(const LoraRows& rows, const ShrinkParams& p, int rank, const Tile& tile,
                                              int k0, int k1, float (&acc)[RT * 2][4]) {
   constexpr int NT = RT * 2;
@@ -104,11 +104,11 @@ __device__ __forceinline__ void few_rows_sum(const LoraRows& rows, const ShrinkP
   }
   const uint16_t* w = p.w + (static_cast<int64_t>(tile.group) * rank + g) * p.len + q * 8;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int k = k0 + warp * 32; k < k1; k += 128 * U) {
+  for (int k = k0 + warp * 32; k < k1; k += 32 * NW * U) {
     uint4 xv[U][2], wv[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = k + u * 128;
+      const int at = k + u * 32 * NW;
       const bool in = at < k1;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -139,7 +139,8 @@ struct FewSmem {
   static constexpr int kWPitch = RP * 2 + 16;
   static constexpr int kStage = kX + 64 * kWPitch;
   static constexpr int kStages = 4;
-  static constexpr int kRed = 80 * RP * 4;  // the tile's sums, and the four warps' behind them
+  // the tile's sums, and the warps' behind them
+  static constexpr int red(int warps) { return (1 + warps) * 16 * RP * 4; }
 };
 
 template <bool BF16, int RT>
@@ -195,7 +196,7 @@ __device__ __forceinline__ void few_rows_staged_sum(const LoraRows& rows, const 
   __syncthreads();
 }
 
-template <bool BF16, int RT, bool KM>
+template <bool BF16, int RT, bool KM, int NW>
 __device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const ShrinkParams& p, int rank, int cs,
                                               const Tile& tile, uint8_t* sm) {
   constexpr int RP = RT * 16, NT = RT * 2;
@@ -211,7 +212,7 @@ __device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const Shrink
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
   if constexpr (KM)
-    few_rows_sum<BF16, RT>(rows, p, rank, tile, s0 * 64, min(s1 * 64, p.len), acc);
+    few_rows_sum<BF16, RT, NW>(rows, p, rank, tile, s0 * 64, min(s1 * 64, p.len), acc);
   else
     few_rows_staged_sum<BF16, RT>(rows, p, rank, tile, s0, s1, sm, acc);
 
@@ -229,12 +230,20 @@ __device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const Shrink
   }
   __syncthreads();
   if (cs > 1) cluster_wait();  // the others have begun
-  for (int at = tid * 4; at < 16 * RP; at += kThreads * 4) {
-    const float4 a = *reinterpret_cast<const float4*>(part + at), b = *reinterpret_cast<const float4*>(part + 16 * RP + at),
-                 c = *reinterpret_cast<const float4*>(part + 32 * RP + at),
-                 d = *reinterpret_cast<const float4*>(part + 48 * RP + at);
-    st_cluster_f32x4(sums_of_row<16, RP>(sums, at / RP, cs, crank) + at % RP * 4, (a.x + b.x) + (c.x + d.x),
-                     (a.y + b.y) + (c.y + d.y), (a.z + b.z) + (c.z + d.z), (a.w + b.w) + (c.w + d.w));
+  for (int at = tid * 4; at < 16 * RP; at += NW * 32 * 4) {
+    float4 v[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v[w] = *reinterpret_cast<const float4*>(part + w * 16 * RP + at);
+#pragma unroll
+    for (int h = NW / 2; h > 0; h /= 2)
+#pragma unroll
+      for (int w = 0; w < h; ++w) {
+        v[w].x += v[w + h].x;
+        v[w].y += v[w + h].y;
+        v[w].z += v[w + h].z;
+        v[w].w += v[w + h].w;
+      }
+    st_cluster_f32x4(sums_of_row<16, RP>(sums, at / RP, cs, crank) + at % RP * 4, v[0].x, v[0].y, v[0].z, v[0].w);
   }
   if (cs > 1) {
     cluster_arrive();
@@ -242,11 +251,15 @@ __device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const Shrink
   } else {
     __syncthreads();
   }
-  finish_rows<BF16, RT, 16, RP>(p, tile, scale, sums, cs, crank, tid);
+  if (tid < kThreads) finish_rows<BF16, RT, 16, RP>(p, tile, scale, sums, cs, crank, tid);
 }
 
+// (staging deals its 64 steps to four warps)
+template <bool BOTH>
+constexpr int kFewWarps = BOTH ? 4 : 8;
+
 template <bool BF16, int RT, bool BOTH>
-__global__ void __launch_bounds__(kThreads) shrink_few_kernel(LoraRows rows, ShrinkParams p0, ShrinkParams p1,
+__global__ void __launch_bounds__(kFewWarps<BOTH> * 32) shrink_few_kernel(LoraRows rows, ShrinkParams p0, ShrinkParams p1,
                                                               int rank, int cs) {
   extern __shared__ __align__(128) uint8_t sm[];
   pdl_wait();
@@ -255,9 +268,9 @@ __global__ void __launch_bounds__(kThreads) shrink_few_kernel(LoraRows rows, Shr
   if (!find_tile(rows, 0, 16, blockIdx.x / cs, tile)) return;  // the same for the whole cluster
   if (cs > 1) cluster_arrive();
   if (!BOTH || blockIdx.y == 0)
-    few_rows_tile<BF16, RT, true>(rows, p0, rank, cs, tile, sm);
+    few_rows_tile<BF16, RT, true, kFewWarps<BOTH>>(rows, p0, rank, cs, tile, sm);
   else
-    few_rows_tile<BF16, RT, false>(rows, p1, rank, cs, tile, sm);
+    few_rows_tile<BF16, RT, false, 4>(rows, p1, rank, cs, tile, sm);
 }
 
 // ------------------------------------------------------------------ many rows
@@ -456,10 +469,10 @@ template <bool BF16, int RT, bool BOTH>
 cudaError_t shrink_few(const LoraRows& rows, const ShrinkParams* p, int rank, int sms, cudaStream_t s) {
   const int64_t tiles = most_tiles(rows.m, rows.adapters, 16);
   const int cs = shares(tiles, p, BOTH ? 2 : 1, 8 * sms);
-  const size_t smem = FewSmem<RT>::kRed + (BOTH ? FewSmem<RT>::kStage * FewSmem<RT>::kStages : 0);
+  const size_t smem = FewSmem<RT>::red(kFewWarps<BOTH>) + (BOTH ? FewSmem<RT>::kStage * FewSmem<RT>::kStages : 0);
   auto kernel = shrink_few_kernel<BF16, RT, BOTH>;
   if (const cudaError_t e = allow_smem(kernel, smem); e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs), BOTH ? 2 : 1), dim3(kThreads), smem, cs, s, rows,
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs), BOTH ? 2 : 1), dim3(kFewWarps<BOTH> * 32), smem, cs, s, rows,
                     p[0], p[BOTH ? 1 : 0], rank, cs);
 }
 
