@@ -289,3 +289,47 @@ def test_beside_a_quantised_projection():
     same = lora.lora_weight_quant_matmul(c.x, W.desc(q), s, c.a, c.b, c.order, c.scale, x3=c.y, stream=side)
     side.synchronize()
     assert torch.equal(got, same)
+
+
+@pytest.mark.parametrize("m", [40, 600])
+def test_chains_of_calls_see_each_others_results(m):
+    """Calls that follow each other with nothing between, each reading what the one before wrote: in place on one
+    tensor, with an order sorted anew into the same memory, and as a replayed graph."""
+    c = Case(m, 256, 640, 16, 5, "bf16", b_std=0.02)
+    ids = [torch.randint(-1, 5, (m,), generator=torch.Generator().manual_seed(s)).cuda() for s in range(4)]
+    want = c.y.clone()
+    for i in range(24):
+        order = lora.adapter_order(ids[i % 4], 5)
+        torch.cuda.synchronize()
+        want = lora.lora_add(c.x, c.a, c.b, order, c.scale, y=want)
+        torch.cuda.synchronize()
+    y, now = c.y.clone(), ids[0].clone()
+
+    def step(i):
+        now.copy_(ids[i % 4])
+        order = lora.adapter_order(now, 5)
+        lora.lora_add(c.x, c.a, c.b, order, c.scale, y=y, out=y)
+
+    for i in range(24):
+        step(i)
+    assert torch.equal(y, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for i in range(4):
+            step(i)
+    for _ in range(3):
+        y.copy_(c.y)
+        for _ in range(6):
+            g.replay()
+        assert torch.equal(y, want)
+    # the gradient of one call as the next one's input
+    grad, all_of = c.grad, []
+    for chained in (False, True):
+        gx, sums = torch.zeros_like(c.x), []
+        for i in range(8):
+            gx, da, db = lora.lora_grad(grad, c.x, c.a, c.b, c.order, c.scale, grad_x=gx, in_place=chained)
+            sums += [da, db]
+            if not chained:
+                torch.cuda.synchronize()
+        all_of.append([gx.clone(), *sums])
+    assert all(torch.equal(p, q) for p, q in zip(*all_of))

@@ -12,6 +12,7 @@ using namespace wqmm;
 namespace {
 
 constexpr int64_t kMaxRank = 128;
+constexpr int64_t kMaxRows = 1 << 30;  // row numbers and the next tile's stay within 32 bits
 
 struct Arg {
   const wqmm_tensor* t;
@@ -48,8 +49,8 @@ wqmm_status check_matrix(const wqmm_tensor* t, const char* name, int64_t* m, int
   const int last = t->ndim - 1;
   *len = t->shape[last];
   *m = t->ndim == 2 ? t->shape[0] : t->shape[0] * t->shape[1];
-  if (*m < 1 || *m > 2147483647LL)
-    return fail(WQMM_ERR_PARAM_INVALID, "%s: %lld rows, not in [1, 2147483647]", name, (long long)*m);
+  if (*m < 1 || *m > kMaxRows)
+    return fail(WQMM_ERR_PARAM_INVALID, "%s: %lld rows, not in [1, %lld]", name, (long long)*m, (long long)kMaxRows);
   if (*len < 1 || *len > 65535 || *len % 32 != 0)
     return fail(WQMM_ERR_PARAM_INVALID, "%s: row length %lld must be a multiple of 32 in [32, 65535]", name,
                 (long long)*len);

@@ -82,14 +82,15 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   struct Item {
     int which, c0, adapter, n, begin, r1;
   };
-  auto item_at = [&](int it) {
+  auto item_at = [&](int it, auto early) {
+    constexpr bool EARLY = decltype(early)::value;
     Item o;
     o.adapter = it / tiles;
     const int ct = it % tiles;
     o.which = ct < tiles0 ? 0 : 1;
     o.c0 = (ct < tiles0 ? ct : ct - tiles0) * 128;
-    const int r0 = offset_at(rows, o.adapter);
-    o.r1 = max(offset_at(rows, o.adapter + 1), r0);
+    const int r0 = offset_at<EARLY>(rows, o.adapter);
+    o.r1 = max(offset_at<EARLY>(rows, o.adapter + 1), r0);
     const int steps = o.r1 > r0 ? (o.r1 - r0 - 1) / 64 + 1 : 0;
     const int s0 = static_cast<int>(static_cast<int64_t>(steps) * crank / cs);
     o.begin = r0 + s0 * 64;
@@ -102,9 +103,9 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   const int xc = tid & 15, xr = (tid >> 4) & 7;
   const uint32_t xto = (xc >> 3) * 8192 + swizzled<128>(xr, xc & 7);
   int number = -1;
-  auto find = [&](const Item& o, int i) {
+  auto find = [&](const Item& o, int i, auto early) {
     const int place = o.begin + i * 64 + 2 * (warp & 3) + (lane & 1) + 8 * ((lane & 15) >> 1);
-    number = i < o.n && place < o.r1 ? rows.source[place] : -1;
+    number = i < o.n && place < o.r1 ? load<decltype(early)::value>(rows.source + place) : -1;
   };
   auto copy_x = [&](const Item& o, int st) {
     const OuterParams& p = o.which == 0 ? p0 : p1;
@@ -169,11 +170,11 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   // before it: the first steps' rows of x are read while it ends, low after that
   int early = 0;
   if (warp < 4 && first < items) {
-    const Item o = item_at(first);
-    find(o, 0);
+    const Item o = item_at(first, std::true_type());
+    find(o, 0, std::true_type());
     for (; early < S && early < o.n; ++early) {
       copy_x(o, early);
-      find(o, early + 1);
+      find(o, early + 1, std::true_type());
     }
   }
   if (SHARED) cluster_arrive();
@@ -195,9 +196,9 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     int g = 0;
     bool live = true;
     for (int it = first; it < items && live; it += stride) {
-      const Item o = item_at(it);
+      const Item o = item_at(it, std::false_type());
       const int had = it == first ? early : 0;
-      if (had == 0) find(o, 0);
+      if (had == 0) find(o, 0, std::false_type());
       for (int i = 0; i < o.n; ++i, ++g) {
         const int st = g % S;
         if (g >= S && !warp_wait(&empty[st], ((g / S) & 1) ^ 1, abort, err, kDevTimeoutProducer)) {
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
         }
         if (i >= had) {
           copy_x(o, st);
-          find(o, i + 1);
+          find(o, i + 1, std::false_type());
         }
         hand_over(&full[st]);
       }
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     int g = 0, k = 0;
     bool live = true;
     for (int it = first; it < items; it += stride, ++k) {
-      const Item o = item_at(it);
+      const Item o = item_at(it, std::false_type());
       float below = 1.f;
       if constexpr (!BF16) {
         // the largest power of two of this CTA's rows
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     int g = 0, k = 0;
     bool live = true;
     for (int it = first; it < items && live; it += stride, ++k) {
-      const Item o = item_at(it);
+      const Item o = item_at(it, std::false_type());
       const int buf = k & 1;
       if (k >= 2 && !warp_wait(&sums_empty[buf], ((k / 2) & 1) ^ 1, abort, err, kDevTimeoutMma)) break;
       tc_fence_after();
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     const int col = quad * 32 + lane;
     int k = 0;
     for (int it = first; it < items; it += stride, ++k) {
-      const Item o = item_at(it);
+      const Item o = item_at(it, std::false_type());
       const OuterParams& p = o.which == 0 ? p0 : p1;
       const int buf = k & 1;
       if (!warp_wait(&sums_full[buf], (k / 2) & 1, abort, err, kDevTimeoutEpilogue)) break;
