@@ -59,6 +59,8 @@ struct OuterParams {
 };
 
 int lora_padded_rank(int rank);
+// Whether the kernels cut these rows into tiles of 16 instead of 128.
+bool lora_few_rows(const LoraRows& rows);
 // x by x k-major weights, and with count 2 then by rank-major ones.
 cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
                                cudaStream_t s);

@@ -491,6 +491,8 @@ cudaError_t shrink_many(const LoraRows& rows, const ShrinkParams* p, int rank, i
 
 int lora_padded_rank(int rank) { return 16 * padded_sixteenths(rank); }
 
+bool lora_few_rows(const LoraRows& rows) { return few_rows(rows); }
+
 cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
                                cudaStream_t s) {
   return with_rank(rank, [&](auto rt) {
