@@ -94,15 +94,6 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 // ------------------------------------------------------------------ tiles of rows
-// EARLY: before pdl_wait().  What a kernel reads there is older than the launch
-// before it, but nothing says that the SM's own cache has dropped its old copy
-// yet, so it is read past that cache.
-template <bool EARLY, typename T>
-__device__ __forceinline__ T load(const T* p) {
-  if constexpr (EARLY) return __ldcg(p);
-  return *p;
-}
-
 // Tile t of the sorted rows when every group of rows is cut into tiles of `bm`:
 // its group and its rows [p0, p1).  The groups are the adapters and, with
 // `bare`, the rows of none behind them.  The offsets are clamped to [0, m], so
@@ -110,12 +101,10 @@ __device__ __forceinline__ T load(const T* p) {
 struct Tile {
   int group, p0, p1;
 };
-template <bool EARLY = false>
 __device__ __forceinline__ int offset_at(const LoraRows& r, int g) {
   const int m = static_cast<int>(r.m);
-  return g > r.adapters ? m : min(max(load<EARLY>(r.offsets + g), 0), m);
+  return g > r.adapters ? m : min(max(r.offsets[g], 0), m);
 }
-template <bool EARLY = false>
 __device__ __forceinline__ bool find_tile(const LoraRows& r, int bare, int bm, int t, Tile& out) {
   const int lane = threadIdx.x & 31;
   const int groups = r.adapters + bare;
@@ -123,8 +112,8 @@ __device__ __forceinline__ bool find_tile(const LoraRows& r, int bare, int bm, i
     const int g = g0 + lane;
     int lo = 0, hi = 0;
     if (g < groups) {
-      lo = offset_at<EARLY>(r, g);
-      hi = offset_at<EARLY>(r, g + 1);
+      lo = offset_at(r, g);
+      hi = offset_at(r, g + 1);
     }
     const int n = hi > lo ? (hi - lo - 1) / bm + 1 : 0;
     int upto = n;
@@ -148,10 +137,9 @@ __device__ __forceinline__ bool find_tile(const LoraRows& r, int bare, int bm, i
   return false;
 }
 // Row of a sorted place, -1 behind the tile (or where the order names no row).
-template <bool EARLY = false>
 __device__ __forceinline__ int row_at(const LoraRows& r, int p, int p1) {
   if (p >= p1) return -1;
-  const int v = load<EARLY>(r.source + p);
+  const int v = r.source[p];
   return v < r.m ? v : -1;
 }
 // Most tiles that m rows in `groups` groups can make.

@@ -30,12 +30,9 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
   const int g = lane >> 2, q = lane & 3;
   const uint32_t base = smem_u32(sm);
   Tile tile;
-  // The launch before this one has waited for all that came before it, and what it
-  // writes itself is low: the order, the weights and y are read while it ends.
-  if (!find_tile<true>(rows, p.bare, BM, blockIdx.x, tile)) {
-    pdl_wait();
-    return;
-  }
+  pdl_wait();
+  pdl_trigger();
+  if (!find_tile(rows, p.bare, BM, blockIdx.x, tile)) return;
   const bool with = tile.group < rows.adapters;
   const uint16_t* w = p.w + static_cast<int64_t>(with ? tile.group : 0) * rank * p.len;
   const int c_begin = blockIdx.y * chunks * 128;
@@ -45,7 +42,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
   uint4 wr[WR][4];
   // k-major: copies under way in shared memory; rank-major: 64 bytes (32 columns) of a rank row per
   // thread and step, in registers until put() changes their words' places
-  auto fetch = [&](int c0, int buf, auto early) {
+  auto fetch = [&](int c0, int buf) {
     if constexpr (KM) {
       const uint32_t ws = base + buf * L::kBuf;
       constexpr int C = RP / 8;
@@ -65,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
         const bool has = r < rank && r < RP && col < c_end;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          wr[i][j] = has ? load<decltype(early)::value>(reinterpret_cast<const uint4*>(w + static_cast<int64_t>(r) * p.len + col + j * 8))
+          wr[i][j] = has ? *reinterpret_cast<const uint4*>(w + static_cast<int64_t>(r) * p.len + col + j * 8)
                          : make_uint4(0, 0, 0, 0);
       }
     }
@@ -87,15 +84,15 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
       }
     }
   };
-  if (with) fetch(c_begin, 0, std::true_type());
+  if (with) fetch(c_begin, 0);
 
   // this thread's two rows: their places in y and out
   const int wrow = WM == 1 ? 0 : warp * 16;
   int row[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) row[i] = row_at<true>(rows, tile.p0 + wrow + g + 8 * i, tile.p1);
+  for (int i = 0; i < 2; ++i) row[i] = row_at(rows, tile.p0 + wrow + g + 8 * i, tile.p1);
   uint4 y[GROUPS][2], next[GROUPS][2];
-  auto fetch_y = [&](int c0, auto early) {
+  auto fetch_y = [&](int c0) {
 #pragma unroll
     for (int s = 0; s < GROUPS; ++s)
 #pragma unroll
@@ -103,12 +100,10 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
         const int col = c0 + (WM == 1 ? warp : s) * 32 + q * 8;
         next[s][i] = make_uint4(0, 0, 0, 0);
         if (p.y.p && row[i] >= 0 && col < c_end)
-          next[s][i] = load<decltype(early)::value>(reinterpret_cast<const uint4*>(p.y.p + row[i] * p.y.ld + col));
+          next[s][i] = *reinterpret_cast<const uint4*>(p.y.p + row[i] * p.y.ld + col);
       }
   };
-  fetch_y(c_begin, std::true_type());
-  pdl_wait();
-  pdl_trigger();
+  fetch_y(c_begin);
 
   float factor[2] = {1.f, 1.f};
   uint32_t a[2][RT][4];  // hi, lo
@@ -133,11 +128,11 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraRows rows, ExpandP
     for (int s = 0; s < GROUPS; ++s)
 #pragma unroll
       for (int i = 0; i < 2; ++i) y[s][i] = next[s][i];
-    if (c0 + 128 < c_end) fetch_y(c0 + 128, std::false_type());
+    if (c0 + 128 < c_end) fetch_y(c0 + 128);
     if (with) {
       put(buf);
       __syncthreads();  // this chunk's weights are there, and the other buffer is read no more
-      if (c0 + 128 < c_end) fetch(c0 + 128, buf ^ 1, std::false_type());
+      if (c0 + 128 < c_end) fetch(c0 + 128, buf ^ 1);
     }
     const uint32_t ws = base + buf * L::kBuf;
 #pragma unroll

@@ -82,15 +82,14 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   struct Item {
     int which, c0, adapter, n, begin, r1;
   };
-  auto item_at = [&](int it, auto early) {
-    constexpr bool EARLY = decltype(early)::value;
+  auto item_at = [&](int it) {
     Item o;
     o.adapter = it / tiles;
     const int ct = it % tiles;
     o.which = ct < tiles0 ? 0 : 1;
     o.c0 = (ct < tiles0 ? ct : ct - tiles0) * 128;
-    const int r0 = offset_at<EARLY>(rows, o.adapter);
-    o.r1 = max(offset_at<EARLY>(rows, o.adapter + 1), r0);
+    const int r0 = offset_at(rows, o.adapter);
+    o.r1 = max(offset_at(rows, o.adapter + 1), r0);
     const int steps = o.r1 > r0 ? (o.r1 - r0 - 1) / 64 + 1 : 0;
     const int s0 = static_cast<int>(static_cast<int64_t>(steps) * crank / cs);
     o.begin = r0 + s0 * 64;
@@ -103,9 +102,9 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   const int xc = tid & 15, xr = (tid >> 4) & 7;
   const uint32_t xto = (xc >> 3) * 8192 + swizzled<128>(xr, xc & 7);
   int number = -1;
-  auto find = [&](const Item& o, int i, auto early) {
+  auto find = [&](const Item& o, int i) {
     const int place = o.begin + i * 64 + 2 * (warp & 3) + (lane & 1) + 8 * ((lane & 15) >> 1);
-    number = i < o.n && place < o.r1 ? load<decltype(early)::value>(rows.source + place) : -1;
+    number = i < o.n && place < o.r1 ? rows.source[place] : -1;
   };
   auto copy_x = [&](const Item& o, int st) {
     const OuterParams& p = o.which == 0 ? p0 : p1;
@@ -166,21 +165,9 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     }
   };
 
-  // x and the order are older than the launch before this one, which has waited for all that came
-  // before it: the first steps' rows of x are read while it ends, low after that
-  int early = 0;
-  if (warp < 4 && first < items) {
-    const Item o = item_at(first, std::true_type());
-    find(o, 0, std::true_type());
-    for (; early < S && early < o.n; ++early) {
-      copy_x(o, early);
-      find(o, early + 1, std::true_type());
-    }
-  }
   if (SHARED) cluster_arrive();
   pdl_wait();
   pdl_trigger();
-  // tensor memory is taken now: the launch before this one may have held it all
   if (warp == 8) {
     tmem_alloc(&tmem_sh, L::kCols);
     tmem_relinquish();
@@ -196,19 +183,16 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     int g = 0;
     bool live = true;
     for (int it = first; it < items && live; it += stride) {
-      const Item o = item_at(it, std::false_type());
-      const int had = it == first ? early : 0;
-      if (had == 0) find(o, 0, std::false_type());
+      const Item o = item_at(it);
+      find(o, 0);
       for (int i = 0; i < o.n; ++i, ++g) {
         const int st = g % S;
         if (g >= S && !warp_wait(&empty[st], ((g / S) & 1) ^ 1, abort, err, kDevTimeoutProducer)) {
           live = false;
           break;
         }
-        if (i >= had) {
-          copy_x(o, st);
-          find(o, i + 1, std::false_type());
-        }
+        copy_x(o, st);
+        find(o, i + 1);
         hand_over(&full[st]);
       }
     }
@@ -220,7 +204,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     int g = 0, k = 0;
     bool live = true;
     for (int it = first; it < items; it += stride, ++k) {
-      const Item o = item_at(it, std::false_type());
+      const Item o = item_at(it);
       float below = 1.f;
       if constexpr (!BF16) {
         // the largest power of two of this CTA's rows
@@ -265,7 +249,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     int g = 0, k = 0;
     bool live = true;
     for (int it = first; it < items && live; it += stride, ++k) {
-      const Item o = item_at(it, std::false_type());
+      const Item o = item_at(it);
       const int buf = k & 1;
       if (k >= 2 && !warp_wait(&sums_empty[buf], ((k / 2) & 1) ^ 1, abort, err, kDevTimeoutMma)) break;
       tc_fence_after();
@@ -302,7 +286,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     const int col = quad * 32 + lane;
     int k = 0;
     for (int it = first; it < items; it += stride, ++k) {
-      const Item o = item_at(it, std::false_type());
+      const Item o = item_at(it);
       const OuterParams& p = o.which == 0 ? p0 : p1;
       const int buf = k & 1;
       if (!warp_wait(&sums_full[buf], (k / 2) & 1, abort, err, kDevTimeoutEpilogue)) break;
