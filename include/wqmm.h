@@ -292,7 +292,7 @@ WQMM_API wqmm_status route_run(void* workspace, uint64_t workspace_size, wqmm_ex
  * lora_get_workspace_size -- low-rank adapters of many requests beside a shared
  * projection, typically a wqmm or qmm output:
  *     output[r] = y[r] + scale[a] * (x1[r] @ lora_a[a]^T) @ lora_b[a]^T,  a the adapter of row r
- *  x1       (m, k) or (b, s, k) float16 or bfloat16, 1 <= m <= 2^30.
+ *  x1       (m, k) or (b, s, k) float16 or bfloat16, 1 <= m <= 2^26.
  *  lora_a   (adapters, rank, k), lora_b (adapters, n, rank): contiguous, dtype of x1.
  *           1 <= adapters <= 2048; rank a multiple of 8 in [8, 128] (pad a smaller one with zeros).
  *  scale    optional (adapters) float32 (NULL: all one).

@@ -12,7 +12,9 @@ using namespace wqmm;
 namespace {
 
 constexpr int64_t kMaxRank = 128;
-constexpr int64_t kMaxRows = 1 << 30;  // row numbers and the next tile's stay within 32 bits
+// Row numbers and the next tile's stay within 32 bits, and one CTA goes through all rows of an adapter in well
+// under the two seconds that a kernel waits for another role.
+constexpr int64_t kMaxRows = 1 << 26;
 
 struct Arg {
   const wqmm_tensor* t;
