@@ -1,6 +1,7 @@
 /*
  * wqmm.h -- C ABI of libwqmm, a B200 (sm_100a) implementation of the compute
- * part of two weight-quantised matmul operators:
+ * part of two weight-quantised matmul operators, and of what stands around them
+ * in a model:
  *
  *   wqmm_*  anti-quant ("pseudo-quant") weight GEMM, after
  *           aclnnWeightQuantMatmulAllReduce ("计算公式"):
@@ -8,6 +9,10 @@
  *   qmm_*   int8 x int8 GEMM, after aclnnQuantMatmulAllReduceV2 ("Function",
  *           cases 1 and 2):
  *             output = dequantScale * pertokenScale * (x1_int8 @ x2_int8 + bias_int32) + x3
+ *   route_*   tokens sorted by expert, copied into that order and summed back with
+ *             weights, and the gradients: around the experts' GEMMs
+ *   lora_*    low-rank adapters of many requests added to a GEMM's output, and
+ *             the gradients
  *
  * The AllReduce of both operators is the identity for one rank and is not
  * performed by these entry points; across ranks (row-parallel, x1 and x2
@@ -30,7 +35,8 @@
  *    launch failure is reported as WQMM_ERR_CUDA (+ message).
  *  - Check order in phase 1 is null -> dtype -> attributes -> shape, as in
  *    "返回值与错误码" of the anti-quant page (CheckNotNull, CheckDtypeValid,
- *    CheckAttr, CheckShape).
+ *    CheckAttr, CheckShape); the routing and adapter operators, which those pages do
+ *    not have, check null -> dtype -> shape.
  *  - Executors are one-shot: phase 2 consumes and frees the executor whether it
  *    succeeds or not ("第二段接口不可重复调用").  An executor that is never run
  *    must be released with wqmm_executor_destroy.
@@ -349,7 +355,8 @@ WQMM_API wqmm_status wqmm_stream_wait(wqmm_stream stream, int32_t timeout_ms);
  * invalid).  Synchronous with respect to the device; `reset` != 0 clears it.
  * Codes: 1 a copy producer, 2 the MMA issuer, 3 a dequantiser, 4 the epilogue
  * (including the wait of a split tile's first owner for the other owners'
- * partials), 5 the final drain of outstanding copies.
+ * partials), 5 the final drain of outstanding copies.  lora_run's kernels with
+ * tensor-core roles (more than 256 rows, and the gradients) report here too.
  * After a timeout, owners that finished late may have left "partial written"
  * flags set in the workspace.  A new wqmm_run call never matches them (each
  * launch waits for a token of its own), but a CUDA graph replays a captured

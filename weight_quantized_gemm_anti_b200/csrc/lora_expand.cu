@@ -12,6 +12,11 @@ namespace {
 // a thread's four results of a 32-column group are neighbours with the next
 // three tiles': column q * 8 + 2 j + e of the group is column 2 q + e of tile
 // j, so a thread adds and stores 16 bytes of a row at once, four threads 64.
+// Results leave the registers that the instruction wrote, with no detour through
+// shared memory; that is why this contraction, over the rank alone, is not a
+// tcgen05 one: at rank 16 its products take 18 % of the time that y and the
+// result need, at rank 64 34 %.  4096 x 4096, rank 16, 67 MB: about 14 us (the
+// memory's floor is 10.4).
 template <int RT, bool KM>
 struct ExpandSmem {
   static constexpr int RP = RT * 16;

@@ -6,8 +6,7 @@
 // copied by four warps with 16-byte asynchronous copies, 128 to 256
 // neighbouring bytes of a row by the lanes next to each other; a gathering
 // tensor copy (four rows of 128 bytes each) moved 7 bytes per clock and SM
-// where 23 are wanted.  A stage's barrier counts the
-// copies as they land.
+// where 23 are wanted.  A stage's barrier counts the copies as they land.
 #pragma once
 #include "lora_common.cuh"
 
