@@ -128,8 +128,9 @@ def test_executors_are_one_shot_and_of_their_own_kind():
     W.wqmm_executor_destroy(ex)
     assert W.route_run(0, 0, ex, 0) == W.ERR_EXECUTOR
     assert W.route_run(0, 0, None, 0) == W.ERR_EXECUTOR
-    st, ws, ex = W.route_sort_get_workspace_size(T((5000, 2), W.DT_I32), 4, T((5,), W.DT_I32), T((10000,), W.DT_I32),
-                                                 T((5000, 2), W.DT_I32))
+    # (more slots than one cluster sorts: the counts need a workspace)
+    st, ws, ex = W.route_sort_get_workspace_size(T((25000, 2), W.DT_I32), 4, T((5,), W.DT_I32), T((50000,), W.DT_I32),
+                                                 T((25000, 2), W.DT_I32))
     assert st == 0 and ws > 0
     assert W.route_run(FAKE, ws - 1, ex, 0) == W.ERR_WORKSPACE  # consumed all the same
     assert W.route_run(FAKE, ws, ex, 0) == W.ERR_EXECUTOR
