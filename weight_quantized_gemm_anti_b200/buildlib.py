@@ -15,7 +15,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libwqmm.so")
 BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["api.cu", "kernels_aux.cu", "kernels_wqmm.cu", "kernels_smallm.cu", "kernels_qmm.cu", "noalloc.cu",
-           "route.cu", "kernels_route.cu", "lora.cu", "lora_shrink.cu", "lora_expand.cu",
+           "route.cu", "kernels_route.cu", "lora.cu", "lora_few.cu", "lora_shrink.cu", "lora_expand.cu",
            "lora_outer.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -1,6 +1,6 @@
 // lora.cu -- phase 1 and phase 2 of the low-rank adapter operators
 // (include/wqmm.h, "low-rank adapters"): argument checks in the order null ->
-// dtype -> attributes -> shape, and plans that launch lora_shrink.cu, lora_expand.cu
+// dtype -> attributes -> shape, and plans that launch lora_few.cu, lora_shrink.cu, lora_expand.cu
 // and lora_outer.cu.
 #include "lora.h"
 
@@ -179,12 +179,18 @@ struct AddPlan final : OpPlan {
   LoraMat y;
   uint16_t* out;
   int64_t ldo;
+  bool few;  // one launch without a workspace
   wqmm_status run(void* workspace, cudaStream_t s) override {
-    const LoraLow low = low_at(p, static_cast<uint8_t*>(workspace));
+    const LoraLow low = few ? LoraLow{} : low_at(p, static_cast<uint8_t*>(workspace));
     const ShrinkParams sp[1] = {{p.x, p.a, p.scale, low, p.k}};
-    cudaError_t e = launch_lora_shrink(p.rows, sp, 1, p.rank, p.bf16, sm_count(), s);
-    if (e != cudaSuccess) return cuda_fail(e, "adapter contraction launch");
     const ExpandParams ep{low, p.b, y, out, ldo, p.n, y.p != out};
+    cudaError_t e;
+    if (few) {
+      e = launch_lora_few(p.rows, sp[0], ep, p.rank, p.bf16, sm_count(), s);
+      return e == cudaSuccess ? WQMM_SUCCESS : cuda_fail(e, "adapter launch");
+    }
+    e = launch_lora_shrink(p.rows, sp, 1, p.rank, p.bf16, sm_count(), s);
+    if (e != cudaSuccess) return cuda_fail(e, "adapter contraction launch");
     e = launch_lora_expand(p.rows, ep, p.rank, false, p.bf16, sm_count(), s);
     return e == cudaSuccess ? WQMM_SUCCESS : cuda_fail(e, "adapter expansion launch");
   }
@@ -245,7 +251,9 @@ wqmm_status add_phase1(const wqmm_tensor* x1, const wqmm_tensor* a, const wqmm_t
     if ((st = check_in_place(y, plan->y.ld, output, plan->ldo, "y"))) return st;
     plan->y.p = static_cast<const uint16_t*>(y->data);
   }
-  return hand_out(OpKind::kLora, std::move(plan), low_bytes(p), workspace_size, executor);
+  plan->few = lora_few_rows(p.rows);
+  const uint64_t workspace = plan->few ? 0 : low_bytes(p);
+  return hand_out(OpKind::kLora, std::move(plan), workspace, workspace_size, executor);
 }
 
 wqmm_status grad_phase1(const wqmm_tensor* grad, const wqmm_tensor* x1, const wqmm_tensor* a, const wqmm_tensor* b,

@@ -1,5 +1,5 @@
-// lora.h -- launchers of the low-rank adapter kernels (lora_shrink.cu,
-// lora_expand.cu, lora_outer.cu) for the
+// lora.h -- launchers of the low-rank adapter kernels (lora_few.cu,
+// lora_shrink.cu, lora_expand.cu, lora_outer.cu) for the
 // host API (lora.cu).  Not part of the public ABI.
 #pragma once
 #include <cuda_runtime.h>
@@ -64,6 +64,9 @@ bool lora_few_rows(const LoraRows& rows);
 // x by x k-major weights, and with count 2 then by rank-major ones.
 cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
                                cudaStream_t s);
+// Both contractions for few rows (sp.out and ep.low are not used).
+cudaError_t launch_lora_few(const LoraRows& rows, const ShrinkParams& sp, const ExpandParams& ep, int rank, bool bf16,
+                            int sms, cudaStream_t s);
 cudaError_t launch_lora_expand(const LoraRows& rows, const ExpandParams& p, int rank, bool rank_major, bool bf16,
                                int sms, cudaStream_t s);
 cudaError_t launch_lora_outer(const LoraRows& rows, const OuterParams (&p)[2], int rank, bool bf16, int sms,

@@ -211,8 +211,10 @@ cudaError_t launch_lora_expand(const LoraRows& rows, const ExpandParams& p, int 
   return with_rank(rank, [&](auto rt) {
     constexpr int RT = decltype(rt)::value;
     auto pick = [&](auto t, auto km) {
-      return few_rows(rows) ? expand_as<decltype(t)::value, RT, decltype(km)::value, 1>(rows, p, rank, sms, s)
-                            : expand_as<decltype(t)::value, RT, decltype(km)::value, 4>(rows, p, rank, sms, s);
+      constexpr bool T = decltype(t)::value, KM = decltype(km)::value;
+      if constexpr (!KM)  // few rows of a forward pass: lora_few.cu
+        if (few_rows(rows)) return expand_as<T, RT, false, 1>(rows, p, rank, sms, s);
+      return expand_as<T, RT, KM, 4>(rows, p, rank, sms, s);
     };
     auto by_major = [&](auto t) { return rank_major ? pick(t, std::false_type()) : pick(t, std::true_type()); };
     return bf16 ? by_major(std::true_type()) : by_major(std::false_type());

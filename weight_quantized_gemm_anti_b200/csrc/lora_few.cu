@@ -1,0 +1,225 @@
+// lora_few.cu -- the low-rank adapters' part for few rows, both contractions in one launch.
+#include "lora_few.cuh"
+
+namespace wqmm {
+namespace {
+
+// A cluster has a tile of 16 rows.  Its CTAs share the contraction over k, send
+// each other their sums, finish the tile's low values (each CTA all of them, the
+// parts added in the order of the CTAs) and share the columns of the result.
+// Eight warps; no operand passes through shared memory but low.  The weights of
+// the columns are read as those of the contraction are: 16 neighbouring bytes of
+// a column's rank per thread, in the order that lets a thread add and store
+// 16 bytes of a row at once (column q * 8 + 2 j + e of a group of 32 is column
+// 2 q + e of the instruction's tile j).  The first columns' weights and y are
+// under way while the sums are exchanged.
+//
+// Latencies bound it: the launch, the order, two rounds of loads, one exchange.
+// One launch and no workspace also spare the host a launch and an allocation.
+constexpr int kWarps = 8;
+
+template <int RT>
+struct FewTile {
+  static constexpr int RP = RT * 16;
+  static constexpr int kLowPitch = 2 * RP + 8;  // 16-bit numbers: rows a bank group apart
+  static constexpr int kSums = 8 * 16 * RP * 4, kPart = kWarps * 16 * RP * 4, kLow = 16 * kLowPitch * 2;
+  static constexpr int kBytes = kSums + kPart + kLow + 64;
+  static constexpr int kGroups = RT == 1 ? 4 : RT == 2 ? 2 : 1;  // of 32 columns, in flight per warp
+  static constexpr int kLoads = RT == 1 ? 1 : RT / 2;            // of a column's rank
+};
+
+template <bool BF16, int RT>
+__global__ void __launch_bounds__(kWarps * 32) few_kernel(LoraRows rows, ShrinkParams sp, ExpandParams p, int rank,
+                                                         int cs) {
+  using L = FewTile<RT>;
+  constexpr int RP = L::RP, NT = RT * 2, U = L::kGroups, KL = L::kLoads;
+  extern __shared__ __align__(128) uint8_t sm[];
+  float* sums = reinterpret_cast<float*>(sm);  // [CTA][16][RP]
+  float* part = reinterpret_cast<float*>(sm + L::kSums);
+  uint16_t* low = reinterpret_cast<uint16_t*>(sm + L::kSums + L::kPart);
+  float* factors = reinterpret_cast<float*>(sm + L::kSums + L::kPart + L::kLow);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  pdl_wait();
+  pdl_trigger();
+  Tile tile;
+  if (!find_tile(rows, p.bare, 16, blockIdx.x / cs, tile)) return;  // the same for the whole cluster
+  const bool with = tile.group < rows.adapters;
+  const int crank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  if (with && cs > 1) cluster_arrive();
+
+  // this thread's two rows of y and out, and its warp's groups of columns
+  int row[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) row[i] = row_at(rows, tile.p0 + g + 8 * i, tile.p1);
+  const int all = p.len / 32;
+  const int g_end = static_cast<int>(static_cast<int64_t>(all) * (crank + 1) / cs);
+  int grp = static_cast<int>(static_cast<int64_t>(all) * crank / cs) + warp;
+  const uint16_t* w = p.w + (static_cast<int64_t>(with ? tile.group : 0) * p.len + (g >> 1) * 8 + (g & 1)) * rank;
+  uint4 wv[U][4][KL], y[U][2];
+  auto fetch = [&] {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = grp + u * kWarps;
+      const bool in = at < g_end;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < KL; ++k) {
+          const int r = RT == 1 ? q * 4 : k * 32 + q * 8;
+          const uint16_t* from = w + (static_cast<int64_t>(at) * 32 + 2 * j) * rank + r;
+          wv[u][j][k] = zero;
+          if (with && in && r < rank) {
+            if constexpr (RT == 1) {
+              const uint2 v = *reinterpret_cast<const uint2*>(from);
+              wv[u][j][k] = make_uint4(v.x, v.y, 0, 0);
+            } else {
+              wv[u][j][k] = *reinterpret_cast<const uint4*>(from);
+            }
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        y[u][i] = in && p.y.p && row[i] >= 0
+                      ? *reinterpret_cast<const uint4*>(p.y.p + row[i] * p.y.ld + at * 32 + q * 8) : zero;
+    }
+  };
+
+  uint32_t a[2][RT][4];  // hi, lo
+  float factor[2] = {1.f, 1.f};
+  if (with) {
+    const float scale = sp.scale ? sp.scale[tile.group] : 1.f;
+    const int steps = sp.len / 32;
+    const int k0 = static_cast<int>(static_cast<int64_t>(steps) * crank / cs) * 32;
+    const int k1 = static_cast<int>(static_cast<int64_t>(steps) * (crank + 1) / cs) * 32;
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    few_rows_sum<BF16, RT, kWarps>(rows, sp, rank, tile, k0, k1, acc);
+    fetch();
+    float* mine = part + warp * 16 * RP;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      *reinterpret_cast<float2*>(mine + g * RP + n * 8 + 2 * q) = make_float2(acc[n][0], acc[n][1]);
+      *reinterpret_cast<float2*>(mine + (g + 8) * RP + n * 8 + 2 * q) = make_float2(acc[n][2], acc[n][3]);
+    }
+    __syncthreads();
+    if (cs > 1) cluster_wait();  // the others have begun
+    for (int at = tid * 4; at < 16 * RP; at += kWarps * 32 * 4) {
+      const float4 v = sum_of_warps<kWarps>(part + at, 16 * RP);
+      const uint32_t to = smem_u32(sums + crank * 16 * RP + at);
+      for (int c = 0; c < cs; ++c) st_cluster_f32x4(cs > 1 ? mapa_shared(to, c) : to, v.x, v.y, v.z, v.w);
+    }
+    if (cs > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+    constexpr int LANES = RP / 4, PER = kWarps * 32 / LANES;
+    for (int r0 = 0; r0 < 16; r0 += PER) {
+      const int r = r0 + tid / LANES, sub = tid % LANES;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (r < 16) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < cs) {
+            const float4 f = *reinterpret_cast<const float4*>(sums + (c * 16 + r) * RP + sub * 4);
+            v[0] += f.x;
+            v[1] += f.y;
+            v[2] += f.z;
+            v[3] += f.w;
+          }
+      }
+      uint2 hi, lo;
+      const float f = split_row<BF16, LANES>(v, scale, hi, lo);
+      if (r < 16) {
+        *reinterpret_cast<uint2*>(low + r * L::kLowPitch + sub * 4) = hi;
+        *reinterpret_cast<uint2*>(low + r * L::kLowPitch + RP + sub * 4) = lo;
+        if (sub == 0) factors[r] = f;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(low + (g + 8 * i) * L::kLowPitch);
+      if constexpr (!BF16) factor[i] = factors[g + 8 * i];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < RT; ++k) {
+          // the words that stand beside the weights' of the same load
+          const int at = h * (RP / 2) + (RT == 1 ? q * 2 : k / 2 * 16 + q * 4 + k % 2 * 2);
+          a[h][k][i] = from[at];
+          a[h][k][i + 2] = from[at + 1];
+        }
+    }
+  } else {
+    fetch();
+  }
+
+  for (; grp < g_end; grp += U * kWarps, fetch()) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int col = (grp + u * kWarps) * 32 + q * 8;
+      float acc[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+      if (with) {
+#pragma unroll
+        for (int k = 0; k < RT; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 v = wv[u][j][RT == 1 ? 0 : k / 2];
+            const uint32_t b0 = k % 2 ? v.z : v.x, b1 = k % 2 ? v.w : v.y;
+            mma<BF16>(acc[j], a[1][k], b0, b1);  // the small part first
+            mma<BF16>(acc[j], a[0][k], b0, b1);
+          }
+      }
+      if (grp + u * kWarps >= g_end) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (row[i] < 0) continue;
+        const uint32_t yv[4] = {y[u][i].x, y[u][i].y, y[u][i].z, y[u][i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float v0 = acc[j][2 * i], v1 = acc[j][2 * i + 1];
+          const float y0 = Half<BF16>::get(yv[j] & 0xffff), y1 = Half<BF16>::get(yv[j] >> 16);
+          v0 = BF16 ? v0 + y0 : fmaf(factor[i], v0, y0);
+          v1 = BF16 ? v1 + y1 : fmaf(factor[i], v1, y1);
+          o[j] = with ? Half<BF16>::put2(v0, v1) : yv[j];
+        }
+        *reinterpret_cast<uint4*>(p.out + row[i] * p.ldo + col) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+}
+
+template <bool BF16, int RT>
+cudaError_t few_as(const LoraRows& rows, const ShrinkParams& sp, const ExpandParams& ep, int rank, int sms,
+                   cudaStream_t s) {
+  const int64_t tiles = most_tiles(rows.m, rows.adapters + ep.bare, 16);
+  int cs = 1;  // as many CTAs per tile as run at once
+  while (cs < 8 && tiles * cs * 2 <= 4 * sms) cs *= 2;
+  auto kernel = few_kernel<BF16, RT>;
+  if (const cudaError_t e = allow_smem(kernel, FewTile<RT>::kBytes); e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs)), dim3(kWarps * 32), FewTile<RT>::kBytes, cs, s,
+                    rows, sp, ep, rank, cs);
+}
+
+}  // namespace
+
+cudaError_t launch_lora_few(const LoraRows& rows, const ShrinkParams& sp, const ExpandParams& ep, int rank, bool bf16,
+                            int sms, cudaStream_t s) {
+  return with_rank(rank, [&](auto rt) {
+    constexpr int RT = decltype(rt)::value;
+    return bf16 ? few_as<true, RT>(rows, sp, ep, rank, sms, s) : few_as<false, RT>(rows, sp, ep, rank, sms, s);
+  });
+}
+
+}  // namespace wqmm

@@ -1,4 +1,5 @@
 // lora_shrink.cu -- the low-rank adapters' contractions over a long axis, low = scale * x W^T.
+#include "lora_few.cuh"
 #include "lora_tc.cuh"
 
 namespace wqmm {
@@ -40,98 +41,21 @@ __device__ __forceinline__ void finish_rows(const ShrinkParams& p, const Tile& t
           v[3] += f.w;
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] *= scale;
-    if constexpr (!BF16) {
-      // largest value of the row (NaN and infinities leave the factor at one)
-      float top = 0.f;
-      bool finite = true;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        top = fmaxf(top, fabsf(v[i]));
-        finite = finite && isfinite(v[i]);
-      }
-      if (!finite) top = __int_as_float(0x7f800000);
-#pragma unroll
-      for (int d = 1; d < LANES; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      // 2^14 <= top * up < 2^15: the exponent's complement, within the normal numbers
-      float up = 1.f;
-      if (top > 0.f && isfinite(top)) {
-        const int e = static_cast<int>(__float_as_uint(top) >> 23);
-        up = __uint_as_float(static_cast<uint32_t>(min(268 - e, 253)) << 23);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] *= up;
-      if (live && sub == 0)
-        p.out.factor[place] = __uint_as_float((254u << 23) - __float_as_uint(up));  // 1 / up, exactly
-    }
+    uint2 hi, lo;
+    const float factor = split_row<BF16, LANES>(v, scale, hi, lo);
     if (live) {
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float a = v[2 * i], b = v[2 * i + 1];
-        hi[i] = Half<BF16>::put2(a, b);
-        const float ha = Half<BF16>::get(hi[i] & 0xffff), hb = Half<BF16>::get(hi[i] >> 16);
-        lo[i] = Half<BF16>::put2(isfinite(ha) ? a - ha : 0.f, isfinite(hb) ? b - hb : 0.f);
-      }
+      if (!BF16 && sub == 0) p.out.factor[place] = factor;
       uint16_t* o = p.out.low + static_cast<int64_t>(place) * (2 * RP) + sub * 4;
-      *reinterpret_cast<uint2*>(o) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(o + RP) = make_uint2(lo[0], lo[1]);
+      *reinterpret_cast<uint2*>(o) = hi;
+      *reinterpret_cast<uint2*>(o + RP) = lo;
     }
   }
 }
 
 // ------------------------------------------------------------------ few rows
-// Tiles of 16 rows: the warps split the contraction, NW of them.  A chain of
-// latencies bounds it: the order, the rows and weights, the cluster's exchange.
-// 16 rows of 16 adapters of rank 16, k = 8192 (4.5 MB): about 4.8 us, of which the
-// loads are 2.8 (four warps; eight take 0.7 us off the whole operator).
-
-// Few rows, k-major weights: nothing is shared between the warps, so the
-// matrix instruction's operands come straight from global memory.  A thread
-// loads 16 bytes of its rows and of its weight rows, eight neighbours of the
-// contraction; four threads' 32 make two steps of the instruction.  Which
-// element stands for which of a step's sixteen does not matter to the sum as
-// long as both operands agree.  Each warp takes every NW-th 32.
-template <bool BF16, int RT, int NW>
-__device__ __forceinline__ void few_rows_sum(const LoraRows& rows, const ShrinkParams& p, int rank, const Tile& tile,
-                                             int k0, int k1, float (&acc)[RT * 2][4]) {
-  constexpr int NT = RT * 2;
-  constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;  // 32s in flight: 10 to 18 loads
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const uint16_t* x[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = row_at(rows, tile.p0 + g + 8 * i, tile.p1);
-    x[i] = r >= 0 ? p.x.p + r * p.x.ld + q * 8 : nullptr;
-  }
-  const uint16_t* w = p.w + (static_cast<int64_t>(tile.group) * rank + g) * p.len + q * 8;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int k = k0 + warp * 32; k < k1; k += 32 * NW * U) {
-    uint4 xv[U][2], wv[U][NT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = k + u * 32 * NW;
-      const bool in = at < k1;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        wv[u][n] = in && n * 8 < rank
-                       ? *reinterpret_cast<const uint4*>(w + static_cast<int64_t>(n) * 8 * p.len + at) : zero;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) xv[u][i] = in && x[i] ? *reinterpret_cast<const uint4*>(x[i] + at) : zero;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t a0[4] = {xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y};
-      const uint32_t a1[4] = {xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w};
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        mma<BF16>(acc[n], a0, wv[u][n].x, wv[u][n].y);
-        mma<BF16>(acc[n], a1, wv[u][n].z, wv[u][n].w);
-      }
-    }
-  }
-}
+// The gradients' two contractions in tiles of 16 rows: four warps split the
+// contraction.  A chain of latencies bounds it: the order, the rows and weights,
+// the cluster's exchange.
 
 // Rank-major weights are staged in shared memory, 64 steps of the contraction at
 // a time, so that the transposing load can make the instruction's operand of them.
@@ -142,8 +66,7 @@ struct FewSmem {
   static constexpr int kWPitch = RP * 2 + 16;
   static constexpr int kStage = kX + 64 * kWPitch;
   static constexpr int kStages = 4;
-  // the tile's sums, and the warps' behind them
-  static constexpr int red(int warps) { return (1 + warps) * 16 * RP * 4; }
+  static constexpr int kRed = 5 * 16 * RP * 4;  // the tile's sums, and the four warps' behind them
 };
 
 template <bool BF16, int RT>
@@ -199,7 +122,7 @@ __device__ __forceinline__ void few_rows_staged_sum(const LoraRows& rows, const 
   __syncthreads();
 }
 
-template <bool BF16, int RT, bool KM, int NW>
+template <bool BF16, int RT, bool KM>
 __device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const ShrinkParams& p, int rank, int cs,
                                               const Tile& tile, uint8_t* sm) {
   constexpr int RP = RT * 16, NT = RT * 2;
@@ -215,7 +138,7 @@ __device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const Shrink
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
   if constexpr (KM)
-    few_rows_sum<BF16, RT, NW>(rows, p, rank, tile, s0 * 64, min(s1 * 64, p.len), acc);
+    few_rows_sum<BF16, RT, 4>(rows, p, rank, tile, s0 * 64, min(s1 * 64, p.len), acc);
   else
     few_rows_staged_sum<BF16, RT>(rows, p, rank, tile, s0, s1, sm, acc);
 
@@ -233,20 +156,9 @@ __device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const Shrink
   }
   __syncthreads();
   if (cs > 1) cluster_wait();  // the others have begun
-  for (int at = tid * 4; at < 16 * RP; at += NW * 32 * 4) {
-    float4 v[NW];
-#pragma unroll
-    for (int w = 0; w < NW; ++w) v[w] = *reinterpret_cast<const float4*>(part + w * 16 * RP + at);
-#pragma unroll
-    for (int h = NW / 2; h > 0; h /= 2)
-#pragma unroll
-      for (int w = 0; w < h; ++w) {
-        v[w].x += v[w + h].x;
-        v[w].y += v[w + h].y;
-        v[w].z += v[w + h].z;
-        v[w].w += v[w + h].w;
-      }
-    st_cluster_f32x4(sums_of_row<16, RP>(sums, at / RP, cs, crank) + at % RP * 4, v[0].x, v[0].y, v[0].z, v[0].w);
+  for (int at = tid * 4; at < 16 * RP; at += kThreads * 4) {
+    const float4 v = sum_of_warps<4>(part + at, 16 * RP);
+    st_cluster_f32x4(sums_of_row<16, RP>(sums, at / RP, cs, crank) + at % RP * 4, v.x, v.y, v.z, v.w);
   }
   if (cs > 1) {
     cluster_arrive();
@@ -254,15 +166,11 @@ __device__ __forceinline__ void few_rows_tile(const LoraRows& rows, const Shrink
   } else {
     __syncthreads();
   }
-  if (tid < kThreads) finish_rows<BF16, RT, 16, RP>(p, tile, scale, sums, cs, crank, tid);
+  finish_rows<BF16, RT, 16, RP>(p, tile, scale, sums, cs, crank, tid);
 }
 
-// (staging deals its 64 steps to four warps)
-template <bool BOTH>
-constexpr int kFewWarps = BOTH ? 4 : 8;
-
-template <bool BF16, int RT, bool BOTH>
-__global__ void __launch_bounds__(kFewWarps<BOTH> * 32) shrink_few_kernel(LoraRows rows, ShrinkParams p0, ShrinkParams p1,
+template <bool BF16, int RT>
+__global__ void __launch_bounds__(kThreads) shrink_few_kernel(LoraRows rows, ShrinkParams p0, ShrinkParams p1,
                                                               int rank, int cs) {
   extern __shared__ __align__(128) uint8_t sm[];
   pdl_wait();
@@ -270,10 +178,10 @@ __global__ void __launch_bounds__(kFewWarps<BOTH> * 32) shrink_few_kernel(LoraRo
   Tile tile;
   if (!find_tile(rows, 0, 16, blockIdx.x / cs, tile)) return;  // the same for the whole cluster
   if (cs > 1) cluster_arrive();
-  if (!BOTH || blockIdx.y == 0)
-    few_rows_tile<BF16, RT, true, kFewWarps<BOTH>>(rows, p0, rank, cs, tile, sm);
+  if (blockIdx.y == 0)
+    few_rows_tile<BF16, RT, true>(rows, p0, rank, cs, tile, sm);
   else
-    few_rows_tile<BF16, RT, false, 4>(rows, p1, rank, cs, tile, sm);
+    few_rows_tile<BF16, RT, false>(rows, p1, rank, cs, tile, sm);
 }
 
 // ------------------------------------------------------------------ many rows
@@ -472,15 +380,15 @@ int shares(int64_t tiles, const ShrinkParams* p, int count, int64_t room) {
   return cs;
 }
 
-template <bool BF16, int RT, bool BOTH>
+template <bool BF16, int RT>
 cudaError_t shrink_few(const LoraRows& rows, const ShrinkParams* p, int rank, int sms, cudaStream_t s) {
   const int64_t tiles = most_tiles(rows.m, rows.adapters, 16);
-  const int cs = shares(tiles, p, BOTH ? 2 : 1, 8 * sms);
-  const size_t smem = FewSmem<RT>::red(kFewWarps<BOTH>) + (BOTH ? FewSmem<RT>::kStage * FewSmem<RT>::kStages : 0);
-  auto kernel = shrink_few_kernel<BF16, RT, BOTH>;
+  const int cs = shares(tiles, p, 2, 8 * sms);
+  constexpr size_t smem = FewSmem<RT>::kRed + FewSmem<RT>::kStage * FewSmem<RT>::kStages;
+  auto kernel = shrink_few_kernel<BF16, RT>;
   if (const cudaError_t e = allow_smem(kernel, smem); e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs), BOTH ? 2 : 1), dim3(kFewWarps<BOTH> * 32), smem, cs, s, rows,
-                    p[0], p[BOTH ? 1 : 0], rank, cs);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs), 2), dim3(kThreads), smem, cs, s, rows, p[0], p[1],
+                    rank, cs);
 }
 
 template <bool BF16, int RT, bool BOTH>
@@ -504,11 +412,11 @@ cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int 
                                cudaStream_t s) {
   return with_rank(rank, [&](auto rt) {
     constexpr int RT = decltype(rt)::value;
-    auto pick = [&](auto t, auto both) {
-      constexpr bool T = decltype(t)::value, B = decltype(both)::value;
-      return few_rows(rows) ? shrink_few<T, RT, B>(rows, p, rank, sms, s) : shrink_many<T, RT, B>(rows, p, rank, sms, s);
+    auto by_count = [&](auto t) {
+      constexpr bool T = decltype(t)::value;
+      if (count == 1) return shrink_many<T, RT, false>(rows, p, rank, sms, s);
+      return few_rows(rows) ? shrink_few<T, RT>(rows, p, rank, sms, s) : shrink_many<T, RT, true>(rows, p, rank, sms, s);
     };
-    auto by_count = [&](auto t) { return count == 2 ? pick(t, std::true_type()) : pick(t, std::false_type()); };
     return bf16 ? by_count(std::true_type()) : by_count(std::false_type());
   });
 }
