@@ -83,11 +83,12 @@ def check(got, want, size, first, second, addend=None):
 
 SHAPES = [(1, 32, 32, 1), (5, 96, 160, 3), (16, 512, 256, 16), (17, 1056, 96, 2), (64, 128, 416, 1), (65, 64, 128, 40),
           (130, 256, 128, 2), (300, 640, 288, 5), (1000, 2048, 1024, 7)]
+MANY = [(1100, 512, 96, 2), (2100, 1024, 416, 3), (4200, 96, 160, 5)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("rank", [8, 16, 24, 64, 72, 128])
-@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("shape", SHAPES + MANY, ids=str)
 def test_add(dtype, rank, shape):
     m, k, n, adapters = shape
     c = Case(m, k, n, rank, adapters, dtype, seed=m + rank)
@@ -144,7 +145,7 @@ def test_no_row_and_every_row_without_adapter(dtype):
             check(g, want, size, *lens, c.gx if g.shape == c.gx.shape else None)
 
 
-@pytest.mark.parametrize("rows", [3, 100])
+@pytest.mark.parametrize("rows", [3, 100, 4200])
 def test_strided_rows_and_three_dimensions(rows):
     """Slices of a fused projection: x1, y and the output are columns of wider matrices, whose others stay."""
     c = Case(rows, 96, 128, 16, 3, "bf16")
@@ -170,7 +171,7 @@ def test_strided_rows_and_three_dimensions(rows):
 
 def test_values_that_are_not_finite_stay_in_their_rows():
     for dtype in ("bf16", "f16"):
-        for m in (40, 200):
+        for m in (40, 200, 4200):
             c = Case(m, 128, 96, 16, 3, dtype, bare=0.3)
             clean = lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=c.y)
             clean_grad = lora.lora_grad(c.grad, c.x, c.a, c.b, c.order, c.scale)
@@ -196,7 +197,7 @@ def test_values_that_are_not_finite_stay_in_their_rows():
 def test_float16_range():
     """x A^T beyond float16's largest number, and gradients below its smallest normal one: what is kept between the
     contractions reaches as far as 32 bits do."""
-    for m in (12, 150):
+    for m in (12, 150, 4200):
         c = Case(m, 256, 96, 16, 2, "f16", x_std=2000.0, a_std=50.0, b_std=1e-6, grad_std=3e-5)
         assert float((c.x.float() @ c.a[0].float().T).abs().max()) > 7e5
         got = lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=c.y)
@@ -216,7 +217,7 @@ def test_float16_range():
 
 def test_orders_that_name_no_row():
     """Entries of the order out of range are skipped: nothing is read or written for them."""
-    for m in (6, 90):
+    for m in (6, 90, 4200):
         c = Case(m, 64, 96, 16, 3, "bf16", bare=0)
         source = c.order.source.clone()
         gone = int(source[2])
@@ -251,7 +252,7 @@ def test_gradients_agree_with_differences():
 
 
 def test_streams_graphs_and_repeats():
-    for m, adapters in ((12, 8), (500, 3)):
+    for m, adapters in ((12, 8), (500, 3), (4200, 3)):
         c = Case(m, 512, 256, 16, adapters, "bf16")
         step = lambda s=None: (lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=c.y, stream=s),
                                *lora.lora_grad(c.grad, c.x, c.a, c.b, c.order, c.scale, grad_x=c.gx, stream=s))
@@ -291,7 +292,7 @@ def test_beside_a_quantised_projection():
     assert torch.equal(got, same)
 
 
-@pytest.mark.parametrize("m", [40, 600])
+@pytest.mark.parametrize("m", [40, 600, 4200])
 def test_chains_of_calls_see_each_others_results(m):
     """Calls that follow each other with nothing between, each reading what the one before wrote: in place on one
     tensor, with an order sorted anew into the same memory, and as a replayed graph."""

@@ -217,7 +217,7 @@ struct GradPlan final : OpPlan {
     // The weights' gradients read x1 and grad again, the input's only back: with many rows the former go first,
     // while x1 and grad are in the L2 cache (4096 x 4096 x 4096: 58 and 62 us); with few the latter, since the
     // former's CTAs can begin beside its last ones (64 rows, 32 adapters: 22 and 29 us).
-    const bool input_first = lora_few_rows(p.rows);
+    const bool input_first = lora_few_rows(p.rows, p.rank);
     if (input_first && (e = input(back, s)) != cudaSuccess) return cuda_fail(e, "adapter input gradient launch");
     const OuterParams op[2] = {{p.x, back, ga, p.k, 1}, {grad, low, gb, p.n, 0}};
     e = launch_lora_outer(p.rows, op, p.rank, p.bf16, sm_count(), s);
@@ -251,7 +251,7 @@ wqmm_status add_phase1(const wqmm_tensor* x1, const wqmm_tensor* a, const wqmm_t
     if ((st = check_in_place(y, plan->y.ld, output, plan->ldo, "y"))) return st;
     plan->y.p = static_cast<const uint16_t*>(y->data);
   }
-  plan->few = lora_few_rows(p.rows);
+  plan->few = lora_one_launch(p.rows, p.rank);
   const uint64_t workspace = plan->few ? 0 : low_bytes(p);
   return hand_out(OpKind::kLora, std::move(plan), workspace, workspace_size, executor);
 }

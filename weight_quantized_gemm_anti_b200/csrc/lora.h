@@ -59,12 +59,14 @@ struct OuterParams {
 };
 
 int lora_padded_rank(int rank);
-// Whether the kernels cut these rows into tiles of 16 instead of 128.
-bool lora_few_rows(const LoraRows& rows);
+// Whether the gradients' kernels cut these rows into tiles of 16 instead of 128.
+bool lora_few_rows(const LoraRows& rows, int rank);
+// Whether a forward pass is launch_lora_few's one launch.
+bool lora_one_launch(const LoraRows& rows, int rank);
 // x by x k-major weights, and with count 2 then by rank-major ones.
 cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
                                cudaStream_t s);
-// Both contractions for few rows (sp.out and ep.low are not used).
+// Both contractions in one launch (sp.out and ep.low are not used).
 cudaError_t launch_lora_few(const LoraRows& rows, const ShrinkParams& sp, const ExpandParams& ep, int rank, bool bf16,
                             int sms, cudaStream_t s);
 cudaError_t launch_lora_expand(const LoraRows& rows, const ExpandParams& p, int rank, bool rank_major, bool bf16,

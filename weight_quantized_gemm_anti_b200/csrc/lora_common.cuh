@@ -159,12 +159,18 @@ cudaError_t with_rank(int rank, F&& f) {
   }
 }
 
-// Whether the rows are cut into tiles of 16 instead of 128: few rows, or few per
-// adapter.  k = n = 4096, the adapters' part, tiles of 16 and of 128 rows, in us:
-//   rank 16, one adapter     64 rows 5.9, 8.5   256 rows 8.1, 9.6   1000 rows 13.8, 11.5
-//   rank 64, one adapter     64 rows 9.7, 12.0  256 rows 13.5, 13.6  400 rows 15.2, 13.7
-//   rank 16, 32 adapters     64 rows 9.4, 13.6  512 rows 13.5, 15.8  1000 rows 17.6, 17.2
-bool few_rows(const LoraRows& r) {
+// Whether a gradient's rows are cut into tiles of 16 instead of 128: few rows, or
+// few per adapter, and at ranks above 64, whose 16-row sums do not fit the
+// registers, the fewest only.  k = n = 4096, the adapters' whole gradient, tiles
+// of 16 and of 128 rows, in us:
+//   rank 16,  one adapter   64 rows 10.2, 13.4  256 rows 14.6, 16.9  512 rows 19.4, 19.1  1000 rows 24.9, 22.6
+//   rank 64,  one adapter   64 rows 18.6, 19.7  256 rows 25.9, 26.7  400 rows 32.1, 28.4
+//   rank 128, one adapter   64 rows 21.3, 24.7  256 rows 47.0, 33.9
+//   rank 16,  32 adapters   64 rows 22.0, 28.8  512 rows 25.0, 36.2  1000 rows 30.3, 37.1
+//   rank 64,  32 adapters   64 rows 43.7, 51.8  512 rows 56.5, 62.2  1000 rows 77.0, 63.5
+//   rank 128, 32 adapters   64 rows 115, 111    512 rows 166, 129
+bool few_rows(const LoraRows& r, int rank) {
+  if (rank > 64) return r.m <= 64;
   return r.m <= 256 || r.m <= 16 * static_cast<int64_t>(r.adapters);
 }
 

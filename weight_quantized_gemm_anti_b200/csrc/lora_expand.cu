@@ -213,7 +213,7 @@ cudaError_t launch_lora_expand(const LoraRows& rows, const ExpandParams& p, int 
     auto pick = [&](auto t, auto km) {
       constexpr bool T = decltype(t)::value, KM = decltype(km)::value;
       if constexpr (!KM)  // few rows of a forward pass: lora_few.cu
-        if (few_rows(rows)) return expand_as<T, RT, false, 1>(rows, p, rank, sms, s);
+        if (few_rows(rows, rank)) return expand_as<T, RT, false, 1>(rows, p, rank, sms, s);
       return expand_as<T, RT, KM, 4>(rows, p, rank, sms, s);
     };
     auto by_major = [&](auto t) { return rank_major ? pick(t, std::false_type()) : pick(t, std::true_type()); };

@@ -4,35 +4,38 @@
 namespace wqmm {
 namespace {
 
+constexpr int kFewWarps = 8;
+
 // A cluster has a tile of 16 rows.  Its CTAs share the contraction over k, send
 // each other their sums, finish the tile's low values (each CTA all of them, the
 // parts added in the order of the CTAs) and share the columns of the result.
-// Eight warps; no operand passes through shared memory but low.  The weights of
+// No operand passes through shared memory but low.  The weights of
 // the columns are read as those of the contraction are: 16 neighbouring bytes of
 // a column's rank per thread, in the order that lets a thread add and store
 // 16 bytes of a row at once (column q * 8 + 2 j + e of a group of 32 is column
 // 2 q + e of the instruction's tile j).  The first columns' weights and y are
 // under way while the sums are exchanged.
 //
-// Latencies bound it: the launch, the order, two rounds of loads, one exchange.
-// One launch and no workspace also spare the host a launch and an allocation.
-constexpr int kWarps = 8;
-
+// Latencies bound few rows: the launch, the order, two rounds of loads, one
+// exchange (k = n = 4096, rank 16: 1 row 4.9 us, 64 rows of four adapters 5.6);
+// many, the reads of the weights, again for each 16 rows (4096 rows: 25 us, 4.0
+// TB/s of x, y and the result).  One launch and no workspace also spare the host a
+// launch and an allocation (8.2 us a call with them, 5.9 without).
 template <int RT>
 struct FewTile {
   static constexpr int RP = RT * 16;
   static constexpr int kLowPitch = 2 * RP + 8;  // 16-bit numbers: rows a bank group apart
-  static constexpr int kSums = 8 * 16 * RP * 4, kPart = kWarps * 16 * RP * 4, kLow = 16 * kLowPitch * 2;
+  static constexpr int kSums = 8 * 16 * RP * 4, kPart = kFewWarps * 16 * RP * 4, kLow = 16 * kLowPitch * 2;
   static constexpr int kBytes = kSums + kPart + kLow + 64;
-  static constexpr int kGroups = RT == 1 ? 4 : RT == 2 ? 2 : 1;  // of 32 columns, in flight per warp
-  static constexpr int kLoads = RT == 1 ? 1 : RT / 2;            // of a column's rank
+  static constexpr int kGroups = RT == 1 ? 2 : 1;      // of 32 columns, in flight per warp
+  static constexpr int kLoads = RT == 1 ? 1 : RT / 2;  // of a column's rank
 };
 
 template <bool BF16, int RT>
-__global__ void __launch_bounds__(kWarps * 32) few_kernel(LoraRows rows, ShrinkParams sp, ExpandParams p, int rank,
-                                                         int cs) {
+__global__ void __launch_bounds__(kFewWarps * 32) few_kernel(LoraRows rows, ShrinkParams sp, ExpandParams p, int rank,
+                                                             int cs) {
   using L = FewTile<RT>;
-  constexpr int RP = L::RP, NT = RT * 2, U = L::kGroups, KL = L::kLoads;
+  constexpr int NW = kFewWarps, RP = L::RP, NT = RT * 2, U = L::kGroups, KL = L::kLoads;
   extern __shared__ __align__(128) uint8_t sm[];
   float* sums = reinterpret_cast<float*>(sm);  // [CTA][16][RP]
   float* part = reinterpret_cast<float*>(sm + L::kSums);
@@ -55,12 +58,12 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(LoraRows rows, ShrinkP
   const int g_end = static_cast<int>(static_cast<int64_t>(all) * (crank + 1) / cs);
   int grp = static_cast<int>(static_cast<int64_t>(all) * crank / cs) + warp;
   const uint16_t* w = p.w + (static_cast<int64_t>(with ? tile.group : 0) * p.len + (g >> 1) * 8 + (g & 1)) * rank;
-  uint4 wv[U][4][KL], y[U][2];
-  auto fetch = [&] {
+  uint4 wv[U][4][KL], y[U][2], wn[U][4][KL], yn[U][2];
+  auto fetch = [&](int grp) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = grp + u * kWarps;
+      const int at = grp + u * NW;
       const bool in = at < g_end;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -68,20 +71,21 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(LoraRows rows, ShrinkP
         for (int k = 0; k < KL; ++k) {
           const int r = RT == 1 ? q * 4 : k * 32 + q * 8;
           const uint16_t* from = w + (static_cast<int64_t>(at) * 32 + 2 * j) * rank + r;
-          wv[u][j][k] = zero;
+          wn[u][j][k] = zero;
           if (with && in && r < rank) {
             if constexpr (RT == 1) {
               const uint2 v = *reinterpret_cast<const uint2*>(from);
-              wv[u][j][k] = make_uint4(v.x, v.y, 0, 0);
+              wn[u][j][k] = make_uint4(v.x, v.y, 0, 0);
             } else {
-              wv[u][j][k] = *reinterpret_cast<const uint4*>(from);
+              wn[u][j][k] = *reinterpret_cast<const uint4*>(from);
             }
           }
         }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        y[u][i] = in && p.y.p && row[i] >= 0
-                      ? *reinterpret_cast<const uint4*>(p.y.p + row[i] * p.y.ld + at * 32 + q * 8) : zero;
+        yn[u][i] = in && p.y.p && row[i] >= 0
+                       ? *reinterpret_cast<const uint4*>(p.y.p + row[i] * p.y.ld + at * 32 + q * 8)
+                       : zero;
     }
   };
 
@@ -97,8 +101,8 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(LoraRows rows, ShrinkP
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    few_rows_sum<BF16, RT, kWarps>(rows, sp, rank, tile, k0, k1, acc);
-    fetch();
+    few_rows_sum<BF16, RT, NW>(rows, sp, rank, tile, k0, k1, acc);
+    fetch(grp);
     float* mine = part + warp * 16 * RP;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -107,8 +111,8 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(LoraRows rows, ShrinkP
     }
     __syncthreads();
     if (cs > 1) cluster_wait();  // the others have begun
-    for (int at = tid * 4; at < 16 * RP; at += kWarps * 32 * 4) {
-      const float4 v = sum_of_warps<kWarps>(part + at, 16 * RP);
+    for (int at = tid * 4; at < 16 * RP; at += NW * 32 * 4) {
+      const float4 v = sum_of_warps<NW>(part + at, 16 * RP);
       const uint32_t to = smem_u32(sums + crank * 16 * RP + at);
       for (int c = 0; c < cs; ++c) st_cluster_f32x4(cs > 1 ? mapa_shared(to, c) : to, v.x, v.y, v.z, v.w);
     }
@@ -118,7 +122,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(LoraRows rows, ShrinkP
     } else {
       __syncthreads();
     }
-    constexpr int LANES = RP / 4, PER = kWarps * 32 / LANES;
+    constexpr int LANES = RP / 4, PER = NW * 32 / LANES;
     for (int r0 = 0; r0 < 16; r0 += PER) {
       const int r = r0 + tid / LANES, sub = tid % LANES;
       float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -157,13 +161,23 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(LoraRows rows, ShrinkP
         }
     }
   } else {
-    fetch();
+    fetch(grp);
   }
 
-  for (; grp < g_end; grp += U * kWarps, fetch()) {
+  for (; grp < g_end; grp += U * NW) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int col = (grp + u * kWarps) * 32 + q * 8;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < KL; ++k) wv[u][j][k] = wn[u][j][k];
+      y[u][0] = yn[u][0];
+      y[u][1] = yn[u][1];
+    }
+    fetch(grp + U * NW);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int col = (grp + u * NW) * 32 + q * 8;
       float acc[4][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -180,7 +194,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(LoraRows rows, ShrinkP
             mma<BF16>(acc[j], a[0][k], b0, b1);
           }
       }
-      if (grp + u * kWarps >= g_end) continue;
+      if (grp + u * NW >= g_end) continue;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (row[i] < 0) continue;
@@ -203,16 +217,41 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(LoraRows rows, ShrinkP
 template <bool BF16, int RT>
 cudaError_t few_as(const LoraRows& rows, const ShrinkParams& sp, const ExpandParams& ep, int rank, int sms,
                    cudaStream_t s) {
-  const int64_t tiles = most_tiles(rows.m, rows.adapters + ep.bare, 16);
-  int cs = 1;  // as many CTAs per tile as run at once
-  while (cs < 8 && tiles * cs * 2 <= 4 * sms) cs *= 2;
   auto kernel = few_kernel<BF16, RT>;
-  if (const cudaError_t e = allow_smem(kernel, FewTile<RT>::kBytes); e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs)), dim3(kWarps * 32), FewTile<RT>::kBytes, cs, s,
-                    rows, sp, ep, rank, cs);
+  constexpr size_t smem = FewTile<RT>::kBytes;
+  if (const cudaError_t e = allow_smem(kernel, smem); e != cudaSuccess) return e;
+  // CTAs of a tile: as many as find room at once, which is seven eighths of the SMs' places, since a cluster's
+  // stay within one group of SMs (rank 64, 256 rows: 136 in clusters of eight 15.8 us, 68 in clusters of four 10.6)
+  const int64_t tiles = most_tiles(rows.m, rows.adapters + ep.bare, 16);
+  const int places = (RT < 4 ? 2 : 1) * sms * 7 / 8;  // by the kernel's registers
+  int cs = 1;
+  while (cs < 8 && tiles * cs * 2 <= places) cs *= 2;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs)), dim3(kFewWarps * 32), smem, cs, s, rows, sp, ep,
+                    rank, cs);
 }
 
 }  // namespace
+
+// The one launch reads an adapter's weights for each 16 of its rows, the two of
+// lora_shrink.cu and lora_expand.cu for each 128 and 64; so the rows up to which
+// it is ahead fall with the rank, and few rows per adapter leave it ahead.
+// k = n = 4096 (4096 x 1024 is more in its favour, 1024 x 8192 less), one launch
+// and two, in us:
+//   one adapter   rank 16  600 rows 9.2, 10.8   2000 rows 14.2, 16.8  4096 rows 25.1, 29.3  8192 rows 50.2, 53.3
+//                 rank 32  600 rows 10.5, 12.7  2000 rows 17.5, 19.4  4096 rows 35.1, 32.1
+//                 rank 64  300 rows 10.7, 14.2  1000 rows 16.5, 18.7  2000 rows 28.0, 26.7
+//                 rank 128 150 rows 14.4, 16.0   300 rows 19.6, 18.8   600 rows 31.2, 21.7
+//   24 adapters   rank 16  2000 rows 14.0, 19.6 4096 rows 26.4, 37.4  8192 rows 50.9, 54.2
+//                 rank 32  2000 rows 18.2, 23.8 4096 rows 36.7, 41.4  8192 rows 71.6, 59.4
+//                 rank 64  600 rows 16.4, 21.5  1000 rows 26.8, 27.0  2000 rows 33.3, 28.9
+//                 rank 128 150 rows 19.8, 28.1   300 rows 32.2, 28.6
+//   64 adapters   rank 64  1000 rows 36.6, 44.1 2000 rows 70.1, 47.7
+//                 rank 128 512 rows 66.2, 70.4  1000 rows 67.2, 81.1
+// (At 1024 x 8192, rank 16 and 8192 rows: 65.9 and 75.5; 4096 x 1024: 29.3 and 27.2.)
+bool lora_one_launch(const LoraRows& r, int rank) {
+  const int64_t most = rank <= 64 ? 65536 / lora_padded_rank(rank) : 256;
+  return r.m <= most || r.m <= 16 * static_cast<int64_t>(r.adapters);
+}
 
 cudaError_t launch_lora_few(const LoraRows& rows, const ShrinkParams& sp, const ExpandParams& ep, int rank, bool bf16,
                             int sms, cudaStream_t s) {

@@ -406,7 +406,7 @@ cudaError_t shrink_many(const LoraRows& rows, const ShrinkParams* p, int rank, i
 
 int lora_padded_rank(int rank) { return 16 * padded_sixteenths(rank); }
 
-bool lora_few_rows(const LoraRows& rows) { return few_rows(rows); }
+bool lora_few_rows(const LoraRows& rows, int rank) { return few_rows(rows, rank); }
 
 cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
                                cudaStream_t s) {
@@ -415,7 +415,8 @@ cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int 
     auto by_count = [&](auto t) {
       constexpr bool T = decltype(t)::value;
       if (count == 1) return shrink_many<T, RT, false>(rows, p, rank, sms, s);
-      return few_rows(rows) ? shrink_few<T, RT>(rows, p, rank, sms, s) : shrink_many<T, RT, true>(rows, p, rank, sms, s);
+      return few_rows(rows, rank) ? shrink_few<T, RT>(rows, p, rank, sms, s)
+                                  : shrink_many<T, RT, true>(rows, p, rank, sms, s);
     };
     return bf16 ? by_count(std::true_type()) : by_count(std::false_type());
   });
