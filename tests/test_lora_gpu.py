@@ -148,12 +148,13 @@ def test_no_row_and_every_row_without_adapter(dtype):
 @pytest.mark.parametrize("rows", [3, 100, 4200])
 def test_strided_rows_and_three_dimensions(rows):
     """Slices of a fused projection: x1, y and the output are columns of wider matrices, whose others stay."""
-    c = Case(rows, 96, 128, 16, 3, "bf16")
+    rank = 24 if rows > 4096 else 16
+    c = Case(rows, 96, 128, rank, 3, "bf16")
     wide_x = torch.randn(rows, 96 + 40, device="cuda").bfloat16()
     wide_y, wide_o = torch.randn(rows, 400, device="cuda").bfloat16(), torch.full((rows, 264), 3.0, device="cuda").bfloat16()
     x, y, out = wide_x[:, 24:120], wide_y[:, 128:256], wide_o[:, 64:192]
     lora.lora_add(x, c.a, c.b, c.order, c.scale, y=y, out=out)
-    check(out, *exact(x, c.a, c.b, c.ids, c.scale, y), 96, 16, y)
+    check(out, *exact(x, c.a, c.b, c.ids, c.scale, y), 96, rank, y)
     assert bool((wide_o[:, :64] == 3).all()) and bool((wide_o[:, 192:] == 3).all())
     before = wide_y.clone()
     lora.lora_add(x, c.a, c.b, c.order, c.scale, y=y, out=y)
@@ -172,7 +173,7 @@ def test_strided_rows_and_three_dimensions(rows):
 def test_values_that_are_not_finite_stay_in_their_rows():
     for dtype in ("bf16", "f16"):
         for m in (40, 200, 4200):
-            c = Case(m, 128, 96, 16, 3, dtype, bare=0.3)
+            c = Case(m, 128, 96, 24 if m > 4096 else 16, 3, dtype, bare=0.3)
             clean = lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=c.y)
             clean_grad = lora.lora_grad(c.grad, c.x, c.a, c.b, c.order, c.scale)
             bare = (c.ids < 0).nonzero()[:, 0].cuda()
@@ -198,27 +199,28 @@ def test_float16_range():
     """x A^T beyond float16's largest number, and gradients below its smallest normal one: what is kept between the
     contractions reaches as far as 32 bits do."""
     for m in (12, 150, 4200):
-        c = Case(m, 256, 96, 16, 2, "f16", x_std=2000.0, a_std=50.0, b_std=1e-6, grad_std=3e-5)
+        rank = 24 if m > 4096 else 16
+        c = Case(m, 256, 96, rank, 2, "f16", x_std=2000.0, a_std=50.0, b_std=1e-6, grad_std=3e-5)
         assert float((c.x.float() @ c.a[0].float().T).abs().max()) > 7e5
         got = lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=c.y)
-        check(got, *exact(c.x, c.a, c.b, c.ids, c.scale, c.y), 256, 16, c.y)
+        check(got, *exact(c.x, c.a, c.b, c.ids, c.scale, c.y), 256, rank, c.y)
         got = lora.lora_grad(c.grad, c.x, c.a, c.b, c.order, c.scale, grad_x=c.gx)
         for g, (want, size), lens in zip(got, exact_grad(c.grad, c.x, c.a, c.b, c.ids, c.scale, c.gx),
-                                         ((96, 16), (96, m), (256, m))):
+                                         ((96, rank), (96, m), (256, m))):
             check(g, want, size, *lens, c.gx if g.shape == c.gx.shape else None)
         # rows of very different sizes in one adapter
         c.x[::2] *= 1e-3
         c.grad[1::3] *= 8e-3
         got = lora.lora_grad(c.grad, c.x, c.a, c.b, c.order, c.scale)
         for g, (want, size), lens in zip(got, exact_grad(c.grad, c.x, c.a, c.b, c.ids, c.scale, None),
-                                         ((96, 16), (96, m), (256, m))):
+                                         ((96, rank), (96, m), (256, m))):
             check(g, want, size, *lens)
 
 
 def test_orders_that_name_no_row():
     """Entries of the order out of range are skipped: nothing is read or written for them."""
     for m in (6, 90, 4200):
-        c = Case(m, 64, 96, 16, 3, "bf16", bare=0)
+        c = Case(m, 64, 96, 24 if m > 4096 else 16, 3, "bf16", bare=0)
         source = c.order.source.clone()
         gone = int(source[2])
         source[2] = m + 5
@@ -253,7 +255,7 @@ def test_gradients_agree_with_differences():
 
 def test_streams_graphs_and_repeats():
     for m, adapters in ((12, 8), (500, 3), (4200, 3)):
-        c = Case(m, 512, 256, 16, adapters, "bf16")
+        c = Case(m, 512, 256, 24 if m > 4096 else 16, adapters, "bf16")
         step = lambda s=None: (lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=c.y, stream=s),
                                *lora.lora_grad(c.grad, c.x, c.a, c.b, c.order, c.scale, grad_x=c.gx, stream=s))
         want = step()
@@ -296,7 +298,7 @@ def test_beside_a_quantised_projection():
 def test_chains_of_calls_see_each_others_results(m):
     """Calls that follow each other with nothing between, each reading what the one before wrote: in place on one
     tensor, with an order sorted anew into the same memory, and as a replayed graph."""
-    c = Case(m, 256, 640, 16, 5, "bf16", b_std=0.02)
+    c = Case(m, 256, 640, 24 if m > 4096 else 16, 5, "bf16", b_std=0.02)
     ids = [torch.randint(-1, 5, (m,), generator=torch.Generator().manual_seed(s)).cuda() for s in range(4)]
     want = c.y.clone()
     for i in range(24):

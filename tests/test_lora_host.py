@@ -38,10 +38,11 @@ def add(**kw):
 
 
 def test_add_accepts():
-    assert add() == (0, 0)  # few rows: one launch, no workspace
-    many = dict(x1=((5000, 64), BF16), source=((5000,), I32), y=((5000, 96), BF16), out=((5000, 96), BF16))
+    assert add() == (0, 0)  # one launch, no workspace
+    many = dict(x1=((5000, 64), BF16), a=((3, 32, 64), BF16), b=((3, 96, 32), BF16), source=((5000,), I32),
+                y=((5000, 96), BF16), out=((5000, 96), BF16))
     st, ws = add(**many)
-    assert st == 0 and ws >= 5000 * 2 * 16 * 2
+    assert st == 0 and ws >= 5000 * 2 * 32 * 2
     assert add(y=None)[0] == 0 and add(scale=None)[0] == 0
     assert add(x1=((2, 3, 64), BF16), y=((2, 3, 96), BF16), out=((6, 96), BF16))[0] == 0
     # slices of wider matrices; three dimensions whose rows are at one stride
@@ -111,7 +112,8 @@ def test_null_pointers():
 
 
 def test_executors_are_one_shot_and_of_their_own_kind():
-    t = {**ADD, "x1": ((5000, 64), BF16), "source": ((5000,), I32), "y": ((5000, 96), BF16), "out": ((5000, 96), BF16)}
+    t = {**ADD, "x1": ((5000, 64), BF16), "a": ((3, 32, 64), BF16), "b": ((3, 96, 32), BF16), "source": ((5000,), I32),
+         "y": ((5000, 96), BF16), "out": ((5000, 96), BF16)}
     args = [T(*t[n]) for n in ("x1", "a", "b", "scale", "offsets", "source", "y", "out")]
     st, ws, ex = W.lora_get_workspace_size(*args)
     assert st == 0

@@ -251,7 +251,7 @@ wqmm_status add_phase1(const wqmm_tensor* x1, const wqmm_tensor* a, const wqmm_t
     if ((st = check_in_place(y, plan->y.ld, output, plan->ldo, "y"))) return st;
     plan->y.p = static_cast<const uint16_t*>(y->data);
   }
-  plan->few = lora_one_launch(p.rows, p.rank);
+  plan->few = lora_one_launch(p.rows, p.rank, plan->y.p != plan->out, sm_count());
   const uint64_t workspace = plan->few ? 0 : low_bytes(p);
   return hand_out(OpKind::kLora, std::move(plan), workspace, workspace_size, executor);
 }

@@ -62,7 +62,7 @@ int lora_padded_rank(int rank);
 // Whether the gradients' kernels cut these rows into tiles of 16 instead of 128.
 bool lora_few_rows(const LoraRows& rows, int rank);
 // Whether a forward pass is launch_lora_few's one launch.
-bool lora_one_launch(const LoraRows& rows, int rank);
+bool lora_one_launch(const LoraRows& rows, int rank, int bare, int sms);
 // x by x k-major weights, and with count 2 then by rank-major ones.
 cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int count, int rank, bool bf16, int sms,
                                cudaStream_t s);

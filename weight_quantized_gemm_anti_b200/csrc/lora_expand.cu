@@ -214,7 +214,8 @@ cudaError_t launch_lora_expand(const LoraRows& rows, const ExpandParams& p, int 
       constexpr bool T = decltype(t)::value, KM = decltype(km)::value;
       if constexpr (!KM)  // few rows of a forward pass: lora_few.cu
         if (few_rows(rows, rank)) return expand_as<T, RT, false, 1>(rows, p, rank, sms, s);
-      return expand_as<T, RT, KM, 4>(rows, p, rank, sms, s);
+      if constexpr (!KM || RT > 1) return expand_as<T, RT, KM, 4>(rows, p, rank, sms, s);
+      return cudaErrorInvalidValue;  // a forward pass at rank 16: lora_few.cu
     };
     auto by_major = [&](auto t) { return rank_major ? pick(t, std::false_type()) : pick(t, std::true_type()); };
     return bf16 ? by_major(std::true_type()) : by_major(std::false_type());

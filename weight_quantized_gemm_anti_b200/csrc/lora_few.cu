@@ -5,6 +5,10 @@ namespace wqmm {
 namespace {
 
 constexpr int kFewWarps = 8;
+// CTAs per SM.  Told to the compiler too: up to rank 32 it then schedules for the registers of two, 23.4 us
+// instead of 25.8 for 4096 rows of 4096 at rank 16.
+template <int RT>
+constexpr int kFewPerSm = RT < 4 ? 2 : 1;
 
 // A cluster has a tile of 16 rows.  Its CTAs share the contraction over k, send
 // each other their sums, finish the tile's low values (each CTA all of them, the
@@ -17,9 +21,9 @@ constexpr int kFewWarps = 8;
 // under way while the sums are exchanged.
 //
 // Latencies bound few rows: the launch, the order, two rounds of loads, one
-// exchange (k = n = 4096, rank 16: 1 row 4.9 us, 64 rows of four adapters 5.6);
-// many, the reads of the weights, again for each 16 rows (4096 rows: 25 us, 4.0
-// TB/s of x, y and the result).  One launch and no workspace also spare the host a
+// exchange (k = n = 4096, rank 16: 1 row 4.9 us, 64 rows of four adapters 5.2);
+// many, memory and the reads of the weights, again for each 16 rows (4096 rows:
+// 22 us, 4.5 TB/s of x, y and the result).  One launch and no workspace also spare the host a
 // launch and an allocation (8.2 us a call with them, 5.9 without).
 template <int RT>
 struct FewTile {
@@ -32,7 +36,8 @@ struct FewTile {
 };
 
 template <bool BF16, int RT>
-__global__ void __launch_bounds__(kFewWarps * 32) few_kernel(LoraRows rows, ShrinkParams sp, ExpandParams p, int rank,
+__global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm<RT>)
+    few_kernel(LoraRows rows, ShrinkParams sp, ExpandParams p, int rank,
                                                              int cs) {
   using L = FewTile<RT>;
   constexpr int NW = kFewWarps, RP = L::RP, NT = RT * 2, U = L::kGroups, KL = L::kLoads;
@@ -214,43 +219,50 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(LoraRows rows, Shri
   }
 }
 
+// Places for CTAs at once: seven eighths of the SMs' (two or one each, by the registers), since a cluster's stay
+// within one group of SMs (rank 64, 256 rows: 136 in clusters of eight 15.8 us, 68 in clusters of four 10.6).
+template <int RT>
+int few_places(int sms) {
+  return kFewPerSm<RT> * sms * 7 / 8;
+}
+
 template <bool BF16, int RT>
 cudaError_t few_as(const LoraRows& rows, const ShrinkParams& sp, const ExpandParams& ep, int rank, int sms,
                    cudaStream_t s) {
   auto kernel = few_kernel<BF16, RT>;
   constexpr size_t smem = FewTile<RT>::kBytes;
   if (const cudaError_t e = allow_smem(kernel, smem); e != cudaSuccess) return e;
-  // CTAs of a tile: as many as find room at once, which is seven eighths of the SMs' places, since a cluster's
-  // stay within one group of SMs (rank 64, 256 rows: 136 in clusters of eight 15.8 us, 68 in clusters of four 10.6)
+  // CTAs of a tile: as many as find room at once
   const int64_t tiles = most_tiles(rows.m, rows.adapters + ep.bare, 16);
-  const int places = (RT < 4 ? 2 : 1) * sms * 7 / 8;  // by the kernel's registers
   int cs = 1;
-  while (cs < 8 && tiles * cs * 2 <= places) cs *= 2;
+  while (cs < 8 && tiles * cs * 2 <= few_places<RT>(sms)) cs *= 2;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(tiles * cs)), dim3(kFewWarps * 32), smem, cs, s, rows, sp, ep,
                     rank, cs);
 }
 
 }  // namespace
 
-// The one launch reads an adapter's weights for each 16 of its rows, the two of
-// lora_shrink.cu and lora_expand.cu for each 128 and 64; so the rows up to which
-// it is ahead fall with the rank, and few rows per adapter leave it ahead.
-// k = n = 4096 (4096 x 1024 is more in its favour, 1024 x 8192 less), one launch
-// and two, in us:
-//   one adapter   rank 16  600 rows 9.2, 10.8   2000 rows 14.2, 16.8  4096 rows 25.1, 29.3  8192 rows 50.2, 53.3
-//                 rank 32  600 rows 10.5, 12.7  2000 rows 17.5, 19.4  4096 rows 35.1, 32.1
-//                 rank 64  300 rows 10.7, 14.2  1000 rows 16.5, 18.7  2000 rows 28.0, 26.7
-//                 rank 128 150 rows 14.4, 16.0   300 rows 19.6, 18.8   600 rows 31.2, 21.7
-//   24 adapters   rank 16  2000 rows 14.0, 19.6 4096 rows 26.4, 37.4  8192 rows 50.9, 54.2
-//                 rank 32  2000 rows 18.2, 23.8 4096 rows 36.7, 41.4  8192 rows 71.6, 59.4
-//                 rank 64  600 rows 16.4, 21.5  1000 rows 26.8, 27.0  2000 rows 33.3, 28.9
-//                 rank 128 150 rows 19.8, 28.1   300 rows 32.2, 28.6
-//   64 adapters   rank 64  1000 rows 36.6, 44.1 2000 rows 70.1, 47.7
-//                 rank 128 512 rows 66.2, 70.4  1000 rows 67.2, 81.1
-// (At 1024 x 8192, rank 16 and 8192 rows: 65.9 and 75.5; 4096 x 1024: 29.3 and 27.2.)
-bool lora_one_launch(const LoraRows& r, int rank) {
-  const int64_t most = rank <= 64 ? 65536 / lora_padded_rank(rank) : 256;
-  return r.m <= most || r.m <= 16 * static_cast<int64_t>(r.adapters);
+// The one launch reads an adapter's weights again for each 16 of its rows, the two
+// of lora_shrink.cu and lora_expand.cu for each 128 and 64.  At rank 16 that costs
+// less than the second launch at any length; above, the rows up to which it is
+// ahead fall with the rank: 4096 at rank 32; at rank 64 as many as make clusters
+// of two CTAs per tile, whose shares of the contraction halve its length; 256 at
+// rank 128.  Few rows per adapter leave it ahead.  k = n = 4096 (4096 x 1024 is
+// more in its favour, 1024 x 8192 less), one launch and two, in us:
+//   one adapter   rank 16  1000 rows 8.5, 11.9   4096 rows 22.2, 29.4  16384 rows 86.8, 95.8
+//                 rank 32  1000 rows 10.3, 14.0  4096 rows 30.4, 32.6   8192 rows 60.5, 56.5
+//                 rank 64   400 rows 10.4, 14.3  1000 rows 15.7, 18.7   1024 rows 20.8, 18.4
+//                 rank 128  150 rows 12.5, 16.1   256 rows 15.2, 18.4    600 rows 31.2, 21.7
+//   24 adapters   rank 16  1000 rows 11.5, 15.6  4096 rows 23.7, 32.3  16384 rows 87.8, 99.5
+//                 rank 32  2048 rows 22.1, 24.1  4096 rows 32.8, 36.8   8192 rows 62.9, 58.7
+//                 rank 64   400 rows 14.6, 22.2  1000 rows 24.4, 23.6   2000 rows 33.3, 28.9
+//                 rank 128  150 rows 19.8, 28.1   300 rows 32.2, 28.6
+//   64 adapters   rank 64  1024 rows 34.3, 40.3  2000 rows 70.1, 47.7
+//                 rank 128  512 rows 66.2, 70.4  1000 rows 67.2, 81.1
+bool lora_one_launch(const LoraRows& r, int rank, int bare, int sms) {
+  if (rank <= 16 || r.m <= 16 * static_cast<int64_t>(r.adapters)) return true;
+  if (rank <= 32) return r.m <= 4096;
+  return rank <= 64 ? most_tiles(r.m, r.adapters + bare, 16) * 2 <= few_places<4>(sms) : r.m <= 256;
 }
 
 cudaError_t launch_lora_few(const LoraRows& rows, const ShrinkParams& sp, const ExpandParams& ep, int rank, bool bf16,

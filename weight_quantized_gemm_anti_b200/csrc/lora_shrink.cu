@@ -414,7 +414,10 @@ cudaError_t launch_lora_shrink(const LoraRows& rows, const ShrinkParams* p, int 
     constexpr int RT = decltype(rt)::value;
     auto by_count = [&](auto t) {
       constexpr bool T = decltype(t)::value;
-      if (count == 1) return shrink_many<T, RT, false>(rows, p, rank, sms, s);
+      if (count == 1) {
+        if constexpr (RT > 1) return shrink_many<T, RT, false>(rows, p, rank, sms, s);
+        return cudaErrorInvalidValue;  // a forward pass at rank 16: lora_few.cu
+      }
       return few_rows(rows, rank) ? shrink_few<T, RT>(rows, p, rank, sms, s)
                                   : shrink_many<T, RT, true>(rows, p, rank, sms, s);
     };
