@@ -305,7 +305,8 @@ WQMM_API wqmm_status route_run(void* workspace, uint64_t workspace_size, wqmm_ex
  *  offsets, source  the rows in the order of their adapters, as route_sort
  *           makes them of one adapter index per row: (adapters + 1) and (m)
  *           int32.  Rows of no adapter (index outside [0, adapters)) get y, or zeros.
- *  y        optional addend, shape of output; may be the output itself (in place).
+ *  y        optional addend, shape of output; may be the output itself (in place),
+ *           and so may x1 where k = n. The output shares no other memory with an input.
  *  output   (m, n) or (b, s, n), dtype of x1.
  * x1, y and output may have any row stride that is a multiple of 8 elements (a
  * slice of a fused projection); every pointer to 16-bit data is 16-byte
@@ -323,7 +324,9 @@ WQMM_API wqmm_status lora_get_workspace_size(const wqmm_tensor* x1, const wqmm_t
  *     grad_b[a] = scale[a] * sum_r grad[r]^T (x1[r] @ lora_a[a]^T)     over the rows r of adapter a
  *  grad       (m, n) or (b, s, n); grad_x optional (NULL: not wanted) and
  *  grad_x_in  optional addend (the projection's own part; may be grad_x itself),
- *             (m, k) or (b, s, k), all of x1's dtype, row strides as above.
+ *             (m, k) or (b, s, k), all of x1's dtype, row strides as above.  grad_x may
+ *             also be x1 or, where k = n, grad (and grad_x_in with it: a residual's
+ *             gradient in place); the outputs share no other memory with an input.
  *  grad_a, grad_b  contiguous, shape and dtype of lora_a and lora_b; zeros for an adapter without rows. */
 WQMM_API wqmm_status lora_grad_get_workspace_size(const wqmm_tensor* grad, const wqmm_tensor* x1,
                                                   const wqmm_tensor* lora_a, const wqmm_tensor* lora_b,
@@ -355,8 +358,9 @@ WQMM_API wqmm_status wqmm_stream_wait(wqmm_stream stream, int32_t timeout_ms);
  * invalid).  Synchronous with respect to the device; `reset` != 0 clears it.
  * Codes: 1 a copy producer, 2 the MMA issuer, 3 a dequantiser, 4 the epilogue
  * (including the wait of a split tile's first owner for the other owners'
- * partials), 5 the final drain of outstanding copies.  lora_run's kernels with
- * tensor-core roles (more than 256 rows, and the gradients) report here too.
+ * partials), 5 the final drain of outstanding copies.  lora_run's kernels on
+ * tcgen05 (forward passes of many rows at ranks above 16, and the gradients) report
+ * here too.
  * After a timeout, owners that finished late may have left "partial written"
  * flags set in the workspace.  A new wqmm_run call never matches them (each
  * launch waits for a token of its own), but a CUDA graph replays a captured

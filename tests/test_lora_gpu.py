@@ -170,6 +170,25 @@ def test_strided_rows_and_three_dimensions(rows):
         assert torch.equal(got.view(100, 128), lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=c.y))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m,rank", [(5, 16), (300, 16), (40, 128), (300, 64), (2100, 64), (4200, 24)])
+def test_in_place_of_an_input(dtype, m, rank):
+    """A residual: the input itself is the addend and the result, and the gradient of the result the input's."""
+    c = Case(m, 288, 288, rank, 4, dtype, b_std=0.02)
+    want = lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=c.x)
+    x = c.x.clone()
+    assert lora.lora_add(x, c.a, c.b, c.order, c.scale, y=x, out=x) is x
+    assert torch.equal(x, want)
+    want = lora.lora_grad(c.grad, c.x, c.a, c.b, c.order, c.scale, grad_x=c.grad)
+    grad = c.grad.clone()
+    got = lora.lora_grad(grad, c.x, c.a, c.b, c.order, c.scale, grad_x=grad, in_place=True)
+    assert got[0] is grad and all(torch.equal(p, q) for p, q in zip(got, want))
+    want = lora.lora_grad(c.grad, c.x, c.a, c.b, c.order, c.scale, grad_x=c.x)
+    x = c.x.clone()
+    got = lora.lora_grad(c.grad, x, c.a, c.b, c.order, c.scale, grad_x=x, in_place=True)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 def test_values_that_are_not_finite_stay_in_their_rows():
     for dtype in ("bf16", "f16"):
         for m in (40, 200, 4200):

@@ -203,6 +203,11 @@ struct GradPlan final : OpPlan {
   int64_t ldgx;
   uint16_t* ga;
   uint16_t* gb;
+  // Whether `in`, rows of `len`, reaches into the memory between grad_x's first row and its last.
+  bool shares(const LoraMat& in, int64_t len) const {
+    const int64_t last = p.rows.m - 1;
+    return gx && in.p < gx + last * ldgx + p.k && gx < in.p + last * in.ld + len;
+  }
   cudaError_t input(const LoraLow& back, cudaStream_t s) const {
     if (!gx) return cudaSuccess;
     const ExpandParams ep{back, p.a, gx_in, gx, ldgx, p.k, gx_in.p != gx};
@@ -217,7 +222,8 @@ struct GradPlan final : OpPlan {
     // The weights' gradients read x1 and grad again, the input's only back: with many rows the former go first,
     // while x1 and grad are in the L2 cache (4096 x 4096 x 4096: 58 and 62 us); with few the latter, since the
     // former's CTAs can begin beside its last ones (64 rows, 32 adapters: 22 and 29 us).
-    const bool input_first = lora_few_rows(p.rows, p.rank);
+    // A grad_x that is x1 or grad itself is written last.
+    const bool input_first = lora_few_rows(p.rows, p.rank) && !shares(p.x, p.k) && !shares(grad, p.n);
     if (input_first && (e = input(back, s)) != cudaSuccess) return cuda_fail(e, "adapter input gradient launch");
     const OuterParams op[2] = {{p.x, back, ga, p.k, 1}, {grad, low, gb, p.n, 0}};
     e = launch_lora_outer(p.rows, op, p.rank, p.bf16, sm_count(), s);
