@@ -160,18 +160,19 @@ cudaError_t with_rank(int rank, F&& f) {
 }
 
 // Whether a gradient's rows are cut into tiles of 16 instead of 128: few rows, or
-// few per adapter, and at ranks above 64, whose 16-row sums do not fit the
-// registers, the fewest only.  k = n = 4096, the adapters' whole gradient, tiles
-// of 16 and of 128 rows, in us:
-//   rank 16,  one adapter   64 rows 10.2, 13.4  256 rows 14.6, 16.9  512 rows 19.4, 19.1  1000 rows 24.9, 22.6
-//   rank 64,  one adapter   64 rows 18.6, 19.7  256 rows 25.9, 26.7  400 rows 32.1, 28.4
-//   rank 128, one adapter   64 rows 21.3, 24.7  256 rows 47.0, 33.9
-//   rank 16,  32 adapters   64 rows 22.0, 28.8  512 rows 25.0, 36.2  1000 rows 30.3, 37.1
-//   rank 64,  32 adapters   64 rows 43.7, 51.8  512 rows 56.5, 62.2  1000 rows 77.0, 63.5
-//   rank 128, 32 adapters   64 rows 115, 111    512 rows 166, 129
+// few per adapter, and the fewer the larger the rank: at 128 the sums of 16
+// rows do not leave the registers enough loads under way.  k = n = 4096 (k = 1024,
+// n = 8192 favours the small tiles, the reverse the large ones), the adapters'
+// whole gradient, tiles of 16 and of 128 rows, in us:
+//   one adapter   rank 16    64 rows 10.3, 13.5  256 rows 14.4, 17.0  512 rows 19.8, 19.6
+//                 rank 64    64 rows 18.6, 20.0  128 rows 21.6, 20.7  256 rows 26.0, 24.6
+//                 rank 128    4 rows 18.0, 25.0   64 rows 21.4, 25.7  128 rows 29.1, 26.4
+//   32 adapters   rank 16    64 rows 20.4, 29.2  512 rows 25.1, 36.4  1000 rows 30.3, 37.1
+//                 rank 64    64 rows 43.9, 52.9  512 rows 57.1, 61.3
+//                 rank 128    4 rows 70.3, 76.2   64 rows 116, 112    512 rows 157, 130
 bool few_rows(const LoraRows& r, int rank) {
   if (rank > 64) return r.m <= 64;
-  return r.m <= 256 || r.m <= 16 * static_cast<int64_t>(r.adapters);
+  return r.m <= (rank <= 32 ? 256 : 128) || r.m <= 16 * static_cast<int64_t>(r.adapters);
 }
 
 }  // namespace

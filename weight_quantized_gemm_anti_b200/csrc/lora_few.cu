@@ -243,26 +243,26 @@ cudaError_t few_as(const LoraRows& rows, const ShrinkParams& sp, const ExpandPar
 }  // namespace
 
 // The one launch reads an adapter's weights again for each 16 of its rows, the two
-// of lora_shrink.cu and lora_expand.cu for each 128 and 64.  At rank 16 that costs
-// less than the second launch at any length; above, the rows up to which it is
-// ahead fall with the rank: 4096 at rank 32; at rank 64 as many as make clusters
-// of two CTAs per tile, whose shares of the contraction halve its length; 256 at
-// rank 128.  Few rows per adapter leave it ahead.  k = n = 4096 (4096 x 1024 is
-// more in its favour, 1024 x 8192 less), one launch and two, in us:
+// of lora_shrink.cu and lora_expand.cu for each 128.  At rank 16 that costs less
+// than the second launch at any length; above, the rows up to which it is ahead
+// fall with the rank: 4096 at rank 32; at rank 64 as many as make clusters of two
+// CTAs per tile, whose shares of the contraction halve its length, and of four
+// at rank 128.  Few rows per adapter leave it ahead.  k = n = 4096 (4096 x 1024
+// is more in its favour, 1024 x 8192 less), one launch and two, in us:
 //   one adapter   rank 16  1000 rows 8.5, 11.9   4096 rows 22.2, 29.4  16384 rows 86.8, 95.8
 //                 rank 32  1000 rows 10.3, 14.0  4096 rows 30.4, 32.6   8192 rows 60.5, 56.5
-//                 rank 64   400 rows 10.4, 14.3  1000 rows 15.7, 18.7   1024 rows 20.8, 18.4
-//                 rank 128  150 rows 12.5, 16.1   256 rows 15.2, 18.4    600 rows 31.2, 21.7
+//                 rank 64   400 rows 10.4, 15.2  1000 rows 15.7, 16.6   1024 rows 20.7, 16.6
+//                 rank 128  150 rows 12.5, 16.7   400 rows 15.5, 18.9    512 rows 21.9, 19.1
 //   24 adapters   rank 16  1000 rows 11.5, 15.6  4096 rows 23.7, 32.3  16384 rows 87.8, 99.5
 //                 rank 32  2048 rows 22.1, 24.1  4096 rows 32.8, 36.8   8192 rows 62.9, 58.7
-//                 rank 64   400 rows 14.6, 22.2  1000 rows 24.4, 23.6   2000 rows 33.3, 28.9
-//                 rank 128  150 rows 19.8, 28.1   300 rows 32.2, 28.6
-//   64 adapters   rank 64  1024 rows 34.3, 40.3  2000 rows 70.1, 47.7
-//                 rank 128  512 rows 66.2, 70.4  1000 rows 67.2, 81.1
+//                 rank 64   512 rows 14.9, 24.5  1000 rows 25.1, 25.4   2000 rows 31.5, 29.5
+//                 rank 128  256 rows 23.7, 30.4   512 rows 25.5, 31.6   1000 rows 47.8, 33.2
+//   64 adapters   rank 64  1024 rows 34.2, 44.2  2000 rows 70.1, 47.7
+//                 rank 128  512 rows 55.9, 72.4  1000 rows 57.4, 73.5
 bool lora_one_launch(const LoraRows& r, int rank, int bare, int sms) {
   if (rank <= 16 || r.m <= 16 * static_cast<int64_t>(r.adapters)) return true;
   if (rank <= 32) return r.m <= 4096;
-  return rank <= 64 ? most_tiles(r.m, r.adapters + bare, 16) * 2 <= few_places<4>(sms) : r.m <= 256;
+  return most_tiles(r.m, r.adapters + bare, 16) * (rank <= 64 ? 2 : 4) <= few_places<4>(sms);
 }
 
 cudaError_t launch_lora_few(const LoraRows& rows, const ShrinkParams& sp, const ExpandParams& ep, int rank, bool bf16,
