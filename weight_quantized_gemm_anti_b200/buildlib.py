@@ -70,7 +70,7 @@ def build_binding(verbose: bool = False) -> str:
     # by nvcc, which links the shared C++ runtime that torch's libraries use
     cmd = [nvcc(), *ARCH, "-O2", "-std=c++17", "-shared", "-cudart", "none", "-Xcompiler", "-fPIC,-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f for d in include for f in ("-isystem", d)),
-           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
            "-lc10_cuda", LIB, "-Xlinker", "-rpath=$ORIGIN"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
