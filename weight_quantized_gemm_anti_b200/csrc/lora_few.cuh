@@ -75,7 +75,9 @@ template <bool BF16, int RT, int NW>
 __device__ __forceinline__ void few_rows_sum(const LoraRows& rows, const ShrinkParams& p, int rank, const Tile& tile,
                                              int k0, int k1, float (&acc)[RT * 2][4]) {
   constexpr int NT = RT * 2;
-  constexpr int U = RT == 1 ? 4 : RT == 2 ? 2 : 1;  // 32s in flight: 10 to 18 loads
+  // 32s in flight: 10 to 20 loads (rank 64 in eight warps, 1000 rows of 4096: two 15.1 us, one 16.1; rank 32 three:
+  // 3 % slower)
+  constexpr int U = RT == 1 ? 4 : RT == 2 || (RT == 4 && NW == 8) ? 2 : 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   const uint16_t* x[2];
 #pragma unroll
