@@ -298,6 +298,28 @@ def test_streams_graphs_and_repeats():
                 assert all(torch.equal(p, q) for p, q in zip(held, want))
 
 
+@pytest.mark.parametrize("ranks", [(16, 64), (64, 128), (24, 24), (128, 8)], ids=str)
+def test_two_streams_at_once(ranks):
+    """Calls of two streams side by side, few and many rows in turn: no call sees another's workspace or sums."""
+    work = []
+    for i, rank in enumerate(ranks):
+        cases = [Case(m, 512, 640, rank, 3, ("bf16", "f16")[i], seed=i) for m in (20, 1500, 4200)]
+        step = lambda c: (lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=c.y),
+                          *lora.lora_grad(c.grad, c.x, c.a, c.b, c.order, c.scale, grad_x=c.gx))
+        work.append((torch.cuda.Stream(), cases, step, [step(c) for c in cases]))
+    torch.cuda.synchronize()
+    got = [[] for _ in work]
+    for turn in range(8):
+        for (stream, cases, step, _), out in zip(work, got):
+            with torch.cuda.stream(stream):
+                out.append([step(c) for c in cases])
+    torch.cuda.synchronize()
+    for (_, _, _, want), out in zip(work, got):
+        for turn in out:
+            for p, q in zip(turn, want):
+                assert all(torch.equal(u, v) for u, v in zip(p, q))
+
+
 def test_beside_a_quantised_projection():
     m, k, n = 37, 256, 128
     c = Case(m, k, n, 16, 4, "bf16")
