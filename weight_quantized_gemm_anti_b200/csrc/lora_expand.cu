@@ -442,7 +442,7 @@ cudaError_t expand_as(const LoraRows& rows, const ExpandParams& p, int rank, int
   constexpr int BM = WM * 16;
   const int64_t tiles = most_tiles(rows.m, rows.adapters + p.bare, BM);
   // columns per CTA: up to 1024, fewer where there would be under two CTAs per SM (4096 x 4096, rank 16: two
-  // CTAs 28.5 us with the contraction before, eight 30.1), or eight of the short-lived ones of few rows
+  // CTAs 28.5 us with a contraction before, eight 30.1), or eight of the short-lived ones of few rows
   const int all = (p.len + 127) / 128;
   int chunks = 8;
   while (chunks > 1 && tiles * ((all + chunks - 1) / chunks) < (WM == 1 ? 8 : 2) * sms) chunks /= 2;

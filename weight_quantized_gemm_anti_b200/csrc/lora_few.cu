@@ -1,4 +1,4 @@
-// lora_few.cu -- the low-rank adapters' part for few rows, both contractions in one launch.
+// lora_few.cu -- the low-rank adapters' part at rank 16 or for few rows, both contractions in one launch.
 #include "lora_few.cuh"
 
 namespace wqmm {
@@ -23,8 +23,8 @@ constexpr int kFewPerSm = RT < 4 ? 2 : 1;
 // Latencies bound few rows: the launch, the order, two rounds of loads, one
 // exchange (k = n = 4096, rank 16: 1 row 4.9 us, 64 rows of four adapters 5.2);
 // many, memory and the reads of the weights, again for each 16 rows (4096 rows:
-// 22 us, 4.5 TB/s of x, y and the result).  One launch and no workspace also spare the host a
-// launch and an allocation (8.2 us a call with them, 5.9 without).
+// 22 us, 4.5 TB/s of x, y and the result).  One launch and no workspace also
+// spare the host a launch and an allocation (8.2 us a call with them, 5.9 without).
 template <int RT>
 struct FewTile {
   static constexpr int RP = RT * 16;

@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(kThreads) shrink_few_kernel(LoraRows rows, Shr
 // rank-major one MN-major.  The copies of x bound the steps (about 800 cycles each,
 // 22 bytes per clock and SM, the memory's rate); the start (2 us until the first
 // stage is there) and the exchange and conversion at the end (2 us) come on top:
-// 4096 rows of 4096, four adapters of rank 16: 13.5 us for 34 MB; both
-// contractions of the gradients, one adapter, 67 MB: 17 us.
+// both contractions of the gradients, 4096 rows of 4096, one adapter of rank 16,
+// 67 MB: 17 us.
 template <int RT>
 struct ShrinkTc {
   static constexpr int RP = RT * 16;

@@ -1,6 +1,6 @@
 // lora_tc.cuh -- what the adapters' tcgen05 kernels (lora_shrink.cu,
-// lora_outer.cu) share: shared-memory operands of both majors and the copies
-// that fill them.
+// lora_expand.cu, lora_outer.cu) share: shared-memory operands of both majors and
+// the copies that fill them.
 //
 // The rows of a tile lie anywhere in x (the order of the adapters), so they are
 // copied by four warps with 16-byte asynchronous copies, 128 to 256
