@@ -377,3 +377,55 @@ def test_chains_of_calls_see_each_others_results(m):
                 torch.cuda.synchronize()
         all_of.append([gx.clone(), *sums])
     assert all(torch.equal(p, q) for p, q in zip(*all_of))
+
+
+def check_float16_rows(got, want, size, first, second, largest, sizes):
+    """As ``check``, for float16 rows of an adapter whose values between the contractions differ widely.  They are
+    kept relative to the largest of them, ``largest``, at 2^15: a value's two numbers are off by at most half of
+    float16's smallest number each, together 2^-24 of what 2^14 or more stand for, 2^-38 of the largest; the sum over
+    the rows by that times the sum of the other factor's ``sizes``."""
+    half = torch.finfo(got.dtype).eps / 2
+    rel = (first / 16 + 8 + 2 * second / 16 + 8) * 2.0 ** -22 + half * half * 1.01 + 4 * 2.0 ** -24
+    slack = size * rel + 2.0 ** -38 * 1.01 * largest * sizes
+    tiny = torch.finfo(got.dtype).smallest_normal * torch.finfo(got.dtype).eps / 2
+    err = (got.cpu().double() - want).abs()
+    bad = ~(err <= slack + half * (want.abs() + slack) + tiny)
+    assert not bool(bad.any()), (float(err.max()), float(want.abs().max()), int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
+def check_float16_weights(c, ranks=slice(None)):
+    """The weights' gradients of a float16 case against 64 bits (of the given rank rows and columns)."""
+    _, da, db = lora.lora_grad(c.grad, c.x, c.a, c.b, c.order, c.scale)
+    _, (wa, sa), (wb, sb) = exact_grad(c.grad, c.x, c.a, c.b, c.ids, c.scale, None)
+    m, k, n = c.x.shape[0], c.x.shape[1], c.grad.shape[1]
+    x, grad = c.x.cpu().double(), c.grad.cpu().double()
+    for i in range(c.a.shape[0]):
+        at, s = (c.ids == i).nonzero()[:, 0], float(c.scale[i])
+        if not len(at):
+            assert not da[i].any() and not db[i].any()
+            continue
+        back, low = s * grad[at] @ c.b[i].cpu().double(), s * x[at] @ c.a[i].cpu().double().T
+        check_float16_rows(da[i][ranks], wa[i][ranks], sa[i][ranks], n, m, float(back[:, ranks].abs().max()),
+                           x[at].abs().sum(0)[None])
+        check_float16_rows(db[i][:, ranks], wb[i][:, ranks], sb[i][:, ranks], k, m, float(low[:, ranks].abs().max()),
+                           grad[at].abs().sum(0)[:, None])
+
+
+#: rows, k, n, rank, adapters: tiles of 16 rows; a cluster's shares of one adapter; several items per CTA
+WEIGHT_PLANS = [(40, 128, 96, 16, 1), (600, 128, 128, 16, 1), (600, 128, 128, 64, 1), (1100, 128, 96, 128, 1),
+                (700, 512, 512, 16, 40)]
+
+
+@pytest.mark.parametrize("plan", WEIGHT_PLANS, ids=str)
+@pytest.mark.parametrize("levels", [(1e-2,), (1e-4,), (1e-6,), (1e-2, 1e-4, 1e-6)], ids=str)
+@pytest.mark.parametrize("small", ["grad", "x", "both"])
+def test_float16_weight_gradients_beside_rows_of_zeros(plan, levels, small):
+    """Masked tokens: rows of the gradient and of the input that are zero take nothing from the others."""
+    m, k, n, rank, adapters = plan
+    c = Case(m, k, n, rank, adapters, "f16", seed=rank + m)
+    row = torch.arange(m)
+    by = torch.tensor(levels)[row % len(levels)].double()
+    of = lambda name: by if small in (name, "both") else torch.ones(m, dtype=torch.float64)
+    c.grad = (c.grad.cpu().double() * torch.where(row % 5 == 1, 0.0, of("grad"))[:, None]).half().cuda()
+    c.x = (c.x.cpu().double() * torch.where(row % 7 == 2, 0.0, of("x"))[:, None]).half().cuda()
+    check_float16_weights(c)

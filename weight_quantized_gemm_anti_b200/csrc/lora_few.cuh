@@ -8,7 +8,9 @@ namespace {
 
 // Four neighbours of a row of low (LANES lanes have the row) times `scale`, as
 // two 16-bit numbers each.  float16: the row is first brought to where its
-// largest value is below 2^15 by a power of two, whose inverse is returned.
+// largest value is below 2^15 by a power of two, whose inverse is returned.  A row of zeros
+// (a masked token's) takes the largest power: its inverse must not be the largest of its adapter's rows,
+// to which the weights' gradients bring them all.
 template <bool BF16, int LANES>
 __device__ __forceinline__ float split_row(float (&v)[4], float scale, uint2& hi, uint2& lo) {
 #pragma unroll
@@ -27,7 +29,7 @@ __device__ __forceinline__ float split_row(float (&v)[4], float scale, uint2& hi
 #pragma unroll
     for (int d = 1; d < LANES; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     // 2^14 <= top * up < 2^15: the exponent's complement, within the normal numbers
-    if (top > 0.f && isfinite(top)) {
+    if (isfinite(top)) {
       const int e = static_cast<int>(__float_as_uint(top) >> 23);
       up = __uint_as_float(static_cast<uint32_t>(min(268 - e, 253)) << 23);
     }
