@@ -327,7 +327,10 @@ WQMM_API wqmm_status lora_get_workspace_size(const wqmm_tensor* x1, const wqmm_t
  *             (m, k) or (b, s, k), all of x1's dtype, row strides as above.  grad_x may
  *             also be x1 or, where k = n, grad (and grad_x_in with it: a residual's
  *             gradient in place); the outputs share no other memory with an input.
- *  grad_a, grad_b  contiguous, shape and dtype of lora_a and lora_b; zeros for an adapter without rows. */
+ *  grad_a, grad_b  contiguous, shape and dtype of lora_a and lora_b; zeros for an adapter without rows.
+ * Precision as above, but in float16's grad_a and grad_b for rows whose scale * (grad @ lora_b), or scale *
+ * (x1 @ lora_a^T), are far below those of other rows of the adapter: they are kept to 2^-38 of the largest
+ * (16 bits of a value down to 2^-22 of it). */
 WQMM_API wqmm_status lora_grad_get_workspace_size(const wqmm_tensor* grad, const wqmm_tensor* x1,
                                                   const wqmm_tensor* lora_a, const wqmm_tensor* lora_b,
                                                   const wqmm_tensor* scale, const wqmm_tensor* offsets,

@@ -429,3 +429,20 @@ def test_float16_weight_gradients_beside_rows_of_zeros(plan, levels, small):
     c.grad = (c.grad.cpu().double() * torch.where(row % 5 == 1, 0.0, of("grad"))[:, None]).half().cuda()
     c.x = (c.x.cpu().double() * torch.where(row % 7 == 2, 0.0, of("x"))[:, None]).half().cuda()
     check_float16_weights(c)
+
+
+@pytest.mark.parametrize("plan", WEIGHT_PLANS, ids=str)
+@pytest.mark.parametrize("apart", [12, 20, 24, 25, 26, 30])
+def test_float16_weight_gradients_of_rows_far_apart(plan, apart):
+    """Rows whose values between the contractions are 2^apart below the others', and whose other factor carries the
+    sum: they lose bits (``check_float16_rows``), not everything."""
+    m, k, n, rank, adapters = plan
+    for low_of_x in (True, False):
+        c = Case(m, k, n, rank, adapters, "f16", bare=0, seed=apart)
+        even = (torch.arange(m) % 2 == 0)[:, None]
+        up, down = 2.0 ** (apart // 2 - 4), 2.0 ** (apart // 2 - 4 - apart)
+        low = torch.where(even, up, down).double()
+        other = torch.where(even, 2.0 ** -14, 1.0).double()  # the rows below: their products are the larger ones
+        x, grad = (low, other) if low_of_x else (other, low)
+        c.x, c.grad = (c.x.cpu().double() * x).half().cuda(), (c.grad.cpu().double() * grad).half().cuda()
+        check_float16_weights(c)

@@ -18,6 +18,8 @@
 // while both products run on the 16-bit matrix instructions.  float16's
 // exponents do not reach as far as 32-bit ones: a row of low is first scaled
 // by a power of two that puts its largest value just below the type's largest.
+// The contraction over the rows, which has one such power for all of them, keeps 2^-38 of the
+// adapter's largest value (the type's smallest number beside 2^14).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

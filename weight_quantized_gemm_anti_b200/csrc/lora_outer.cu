@@ -12,7 +12,8 @@ namespace {
 // Roles: four warps copy the rows of x (in the order of their adapters), four
 // those of low, one issues the MMAs, four write the sums.  Rows behind the adapter's last
 // are zeros in both operands.  float16 rows of low have a power of two each;
-// on their way to shared memory they are brought to the largest of the CTA's rows.
+// on their way to shared memory they are brought to the largest of the CTA's rows,
+// where a value's two numbers are off by 2^-25 each: 2^-38 of the largest value.
 //
 // An item is 128 columns of one adapter's gradient.  With few items a cluster
 // shares one, each CTA a part of the rows, and the parts meet in shared memory
@@ -161,11 +162,21 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   auto store_low = [&](int st, float below) {
 #pragma unroll
     for (int j = 0; j < (BF16 ? 0 : kLowChunks); ++j) {
-      const __half2 by = __float2half2_rn(held_by[j] * below);
+      // the row's power of two beside the largest: exact in 16 bits down to 2^-24, below it multiplies in 32 (the
+      // least of them keeps an infinity's product one); either way each number is rounded once
+      const float ratio = fmaxf(held_by[j] * below, 0x1p-126f);
+      const __half2 by = __float2half2_rn(ratio);
       uint32_t w[4] = {held[j].x, held[j].y, held[j].z, held[j].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&w[k]), by);
+        const __half2 u = *reinterpret_cast<const __half2*>(&w[k]);
+        __half2 v;
+        if (ratio >= 0x1p-24f) {
+          v = __hmul2(u, by);
+        } else {
+          const float2 f = __half22float2(u);
+          v = __floats2half2_rn(f.x * ratio, f.y * ratio);
+        }
         w[k] = *reinterpret_cast<const uint32_t*>(&v);
       }
       *reinterpret_cast<uint4*>(sm + low_to(st, j)) = make_uint4(w[0], w[1], w[2], w[3]);
