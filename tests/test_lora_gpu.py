@@ -446,3 +446,39 @@ def test_float16_weight_gradients_of_rows_far_apart(plan, apart):
         x, grad = (low, other) if low_of_x else (other, low)
         c.x, c.grad = (c.x.cpu().double() * x).half().cuda(), (c.grad.cpu().double() * grad).half().cuda()
         check_float16_weights(c)
+
+
+@pytest.mark.parametrize("plan", WEIGHT_PLANS, ids=str)
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_float16_weight_gradients_beside_a_rank_that_is_not_finite(plan, value):
+    """One rank row of A and column of B with a value that is not finite: the other ranks' gradients keep their bits,
+    of small values and of values beyond float16's largest."""
+    m, k, n, rank, adapters = plan
+    others = [r for r in range(rank) if r != 3]
+    for grad_std, b_std, x_std, a_std in ((1e-4, 0.1, 1.0, None), (1e3, 100.0, 1e-5, 0.1), (1e-5, 0.1, 1e3, 100.0)):
+        c = Case(m, k, n, rank, adapters, "f16", seed=m, x_std=x_std, a_std=a_std, b_std=b_std, grad_std=grad_std)
+        c.a[:, 3, 7], c.b[:, 9, 3] = value, value
+        _, da, db = lora.lora_grad(c.grad, c.x, c.a, c.b, c.order, c.scale)
+        for i in c.ids.unique().tolist():
+            if i >= 0:
+                assert not bool(torch.isfinite(da[i, 3]).any() or torch.isfinite(db[i, :, 3]).any())
+        check_float16_weights(c, others)
+
+
+def test_float16_infinities_come_through():
+    """A row whose only values between the contractions are infinite, beside rows of ordinary ones."""
+    for m in (20, 600):
+        c = Case(m, 128, 96, 16, 1, "f16", bare=0)
+        c.a[0, :, 40] = 0
+        c.a[0, 3, 40] = float("inf")
+        c.x[:, 40] = c.x[:, 40].abs() + 0.5
+        c.x[5] = 0
+        c.x[5, 40] = 1
+        c.grad[:, :4] = c.grad[:, :4].abs() + 0.5
+        _, _, db = lora.lora_grad(c.grad, c.x, c.a, c.b, c.order, c.scale)
+        assert bool((db[0, :4, 3] == float("inf")).all())
+        assert bool(torch.isfinite(db[0][:, [r for r in range(16) if r != 3]]).all())
+        c.b[0, 2] = 0
+        c.b[0, 2, 3] = 1
+        out = lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=c.y)
+        assert bool((out[:, 2] == float("inf")).all())

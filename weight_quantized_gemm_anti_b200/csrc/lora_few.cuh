@@ -8,31 +8,25 @@ namespace {
 
 // Four neighbours of a row of low (LANES lanes have the row) times `scale`, as
 // two 16-bit numbers each.  float16: the row is first brought to where its
-// largest value is below 2^15 by a power of two, whose inverse is returned.  A row of zeros
+// largest finite value is below 2^15 by a power of two, whose inverse is returned.  A row of zeros
 // (a masked token's) takes the largest power: its inverse must not be the largest of its adapter's rows,
-// to which the weights' gradients bring them all.
+// to which the weights' gradients bring them all.  Values that are not finite stay so under any power;
+// beside them the row's others keep their bits.
 template <bool BF16, int LANES>
 __device__ __forceinline__ float split_row(float (&v)[4], float scale, uint2& hi, uint2& lo) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] *= scale;
   float up = 1.f;
   if constexpr (!BF16) {
-    // largest value of the row (NaN and infinities leave the factor at one)
+    // the row's largest value, NaN and infinities aside
     float top = 0.f;
-    bool finite = true;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      top = fmaxf(top, fabsf(v[i]));
-      finite = finite && isfinite(v[i]);
-    }
-    if (!finite) top = __int_as_float(0x7f800000);
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, isfinite(v[i]) ? fabsf(v[i]) : 0.f);
 #pragma unroll
     for (int d = 1; d < LANES; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     // 2^14 <= top * up < 2^15: the exponent's complement, within the normal numbers
-    if (isfinite(top)) {
-      const int e = static_cast<int>(__float_as_uint(top) >> 23);
-      up = __uint_as_float(static_cast<uint32_t>(min(268 - e, 253)) << 23);
-    }
+    const int e = static_cast<int>(__float_as_uint(top) >> 23);
+    up = __uint_as_float(static_cast<uint32_t>(min(268 - e, 253)) << 23);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] *= up;
   }
