@@ -306,7 +306,8 @@ WQMM_API wqmm_status route_run(void* workspace, uint64_t workspace_size, wqmm_ex
  *           makes them of one adapter index per row: (adapters + 1) and (m)
  *           int32.  Rows of no adapter (index outside [0, adapters)) get y, or zeros.
  *  y        optional addend, shape of output; may be the output itself (in place),
- *           and so may x1 where k = n. The output shares no other memory with an input.
+ *           and so may x1 where k = n.  The output shares no other memory with an input
+ *           (columns of one matrix are apart); phase 2 refuses it before any launch.
  *  output   (m, n) or (b, s, n), dtype of x1.
  * x1, y and output may have any row stride that is a multiple of 8 elements (a
  * slice of a fused projection); every pointer to 16-bit data is 16-byte
@@ -326,7 +327,8 @@ WQMM_API wqmm_status lora_get_workspace_size(const wqmm_tensor* x1, const wqmm_t
  *  grad_x_in  optional addend (the projection's own part; may be grad_x itself),
  *             (m, k) or (b, s, k), all of x1's dtype, row strides as above.  grad_x may
  *             also be x1 or, where k = n, grad (and grad_x_in with it: a residual's
- *             gradient in place); the outputs share no other memory with an input.
+ *             gradient in place); the outputs share no other memory with an input or each other
+ *             (phase 2 refuses it).
  *  grad_a, grad_b  contiguous, shape and dtype of lora_a and lora_b; zeros for an adapter without rows.
  * Precision as above, but in float16's grad_a and grad_b for rows whose scale * (grad @ lora_b), or scale *
  * (x1 @ lora_a^T), are far below those of other rows of the adapter: they are kept to 2^-38 of the largest

@@ -482,3 +482,26 @@ def test_float16_infinities_come_through():
         c.b[0, 2, 3] = 1
         out = lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=c.y)
         assert bool((out[:, 2] == float("inf")).all())
+
+
+@pytest.mark.parametrize("rows,rank", [(1, 16), (100, 16), (4200, 24)])
+def test_columns_of_one_matrix(rows, rank):
+    """x1, the addend in the result's place, the gradients and what they are of as columns of one matrix: nothing in
+    common.  Columns in common are refused, before anything is written."""
+    c = Case(rows, 96, 96, rank, 3, "bf16")
+    wide = torch.randn(rows, 320, device="cuda").bfloat16()
+    x, y, third = wide[:, :96], wide[:, 96:192], wide[:, 200:296]
+    before = wide.clone()
+    want = lora.lora_add(x.clone(), c.a, c.b, c.order, c.scale, y=y.clone())
+    lora.lora_add(x, c.a, c.b, c.order, c.scale, y=y, out=y)
+    assert torch.equal(y, want)
+    want = lora.lora_grad(y.clone(), x.clone(), c.a, c.b, c.order, c.scale, grad_x=third.clone())
+    got = lora.lora_grad(y, x, c.a, c.b, c.order, c.scale, grad_x=third, in_place=True)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert torch.equal(wide[:, :96], before[:, :96]) and torch.equal(wide[:, 296:], before[:, 296:])
+    now = wide.clone()
+    with pytest.raises(W.WqmmError, match="shares memory"):
+        lora.lora_add(x, c.a, c.b, c.order, c.scale, out=wide[:, 88:184])
+    with pytest.raises(W.WqmmError, match="shares memory"):
+        lora.lora_grad(y, x, c.a, c.b, c.order, c.scale, grad_x=wide[:, 184:280], in_place=True)
+    assert torch.equal(wide, now)

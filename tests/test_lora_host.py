@@ -132,3 +132,63 @@ def test_wrappers_refuse():
               lambda: lora.lora_weight_quant_matmul(x, W.desc(a[0]), None, a, b, order)):
         with pytest.raises(ValueError, match="CUDA"):
             f()
+
+
+# ------------------------------------------------------------------ memory that an output shares
+# Phase 2 refuses it before it launches; the addresses are made up, so only where no GPU could be given them.
+torch = pytest.importorskip("torch")
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses")
+BIG = 1 << 20  # apart: each tensor has a megabyte of its own
+
+
+def run_at(phase1, names, table, at, **kw):
+    """Phase 2's status with tensor i at BIG * (i + 1), or where `at` says (bytes from there)."""
+    t = {**table, **kw}
+    descs = []
+    for i, n in enumerate(names):
+        if t[n] is None:
+            descs.append(None)
+            continue
+        base, off = at.get(n, (n, 0))
+        extra = t[n][2] if len(t[n]) > 2 else {}
+        descs.append(T(*t[n][:2], data=BIG * (names.index(base) + 1) + off, **extra))
+    st, ws, ex = phase1(*descs)
+    assert st == 0, W.wqmm_last_error()
+    return W.lora_run(BIG * 64, ws, ex, 0)
+
+
+ADD_NAMES = ["x1", "a", "b", "scale", "offsets", "source", "y", "out"]
+SQUARE = dict(x1=((6, 64), BF16), b=((3, 64, 16), BF16), y=((6, 64), BF16), out=((6, 64), BF16))
+WIDE = lambda ld, n=64: ((6, n), BF16, dict(strides=(ld, 1)))
+
+
+@no_gpu
+@pytest.mark.parametrize("at,kw", [
+    (dict(out=("x1", 0)), {}),  # k and n differ
+    (dict(out=("x1", 0)), dict(SQUARE, x1=WIDE(128))), (dict(out=("x1", 0)), dict(SQUARE, out=WIDE(128))),
+    (dict(out=("x1", 16)), SQUARE), (dict(out=("x1", 128)), SQUARE), (dict(out=("y", 16)), SQUARE),
+    (dict(out=("y", 128)), SQUARE), (dict(y=("out", 128)), SQUARE), (dict(out=("x1", 6 * 128 - 16)), SQUARE),
+    (dict(out=("x1", 112)), dict(SQUARE, x1=WIDE(128), out=WIDE(128))),  # columns of one matrix, eight in common
+    (dict(x1=("out", 144)), dict(SQUARE, x1=WIDE(128), out=WIDE(128))),  # reaches into the next row's
+    (dict(out=("a", 32)), {}), (dict(out=("b", 0)), {}), (dict(out=("scale", 0)), {}), (dict(out=("offsets", 0)), {}),
+    (dict(source=("out", 1136)), {}), (dict(out=("x1", 0)), dict(x1=((1, 64), BF16), source=((1,), I32),
+                                                              y=((1, 96), BF16), out=((1, 96), BF16)))])
+def test_add_refuses_memory_in_common(at, kw):
+    assert run_at(W.lora_get_workspace_size, ADD_NAMES, ADD, at, **kw) == INVALID
+    assert "shares memory" in W.wqmm_last_error()
+
+
+GRAD_SQUARE = dict(grad=((6, 64), BF16), b=((3, 64, 16), BF16), gb=((3, 64, 16), BF16))
+
+
+@no_gpu
+@pytest.mark.parametrize("at,kw", [
+    (dict(gx=("grad", 0)), {}), (dict(gx=("x1", 16)), GRAD_SQUARE), (dict(gx=("grad", 16)), GRAD_SQUARE),
+    (dict(gx=("x1", 0)), dict(GRAD_SQUARE, gx=WIDE(72), gx_in=None)),
+    (dict(gx=("grad", 0)), dict(GRAD_SQUARE, grad=WIDE(72))), (dict(gx=("gx_in", 128)), {}),
+    (dict(gx=("a", 0)), {}), (dict(ga=("a", 0)), {}), (dict(gb=("b", 0)), {}), (dict(ga=("x1", 0)), {}),
+    (dict(gb=("grad", 64)), {}), (dict(ga=("gb", 16)), {}), (dict(gx=("ga", 16)), {}), (dict(gb=("gx_in", 0)), {}),
+    (dict(ga=("source", 0)), {}), (dict(ga=("scale", 0)), {})])
+def test_grad_refuses_memory_in_common(at, kw):
+    assert run_at(W.lora_grad_get_workspace_size, list(GRAD), GRAD, at, **kw) == INVALID
+    assert "shares memory" in W.wqmm_last_error()

@@ -176,6 +176,19 @@ const char* dt_name(int dt) {
   }
 }
 
+int dt_bytes(int dt) {
+  switch (dt) {
+    case WQMM_DT_I8:
+    case WQMM_DT_FP8E4M3: return 1;
+    case WQMM_DT_F16:
+    case WQMM_DT_BF16: return 2;
+    case WQMM_DT_F32:
+    case WQMM_DT_I32: return 4;
+    case WQMM_DT_I64: return 8;
+    default: return 0;
+  }
+}
+
 wqmm_status check_descriptor(const wqmm_tensor* t, const char* name) {
   if (t->ndim < 1 || t->ndim > 3) return fail(WQMM_ERR_PARAM_INVALID, "%s: ndim %d not in [1, 3]", name, t->ndim);
   if (t->reserved != 0) return fail(WQMM_ERR_PARAM_INVALID, "%s: reserved field must be 0", name);
@@ -1065,11 +1078,48 @@ wqmm_status hand_out(OpKind op, std::unique_ptr<OpPlan> plan, uint64_t workspace
   return ok();
 }
 
+Memory whole(const wqmm_tensor* t, const char* name, int may_be) {
+  const int64_t bytes = numel(t) * dt_bytes(t->dtype);
+  return {name, t->data, 1, bytes, bytes, may_be};
+}
+
+namespace {
+
+// Whether two tensors have a byte in common.  Rows at one stride (columns of one wider matrix) are told apart by their
+// place in it; rows at different strides that reach into each other count as sharing.
+bool share(Memory a, Memory b) {
+  if (!a.p || !b.p || a.rows * a.len == 0 || b.rows * b.len == 0) return false;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  if (pa >= pb + (b.rows - 1) * b.ld + b.len || pb >= pa + (a.rows - 1) * a.ld + a.len) return false;
+  if (a.rows == 1) a.ld = b.ld;  // a single row is at any stride
+  if (b.rows == 1) b.ld = a.ld;
+  if (a.ld != b.ld) return true;
+  const int64_t ld = a.ld, d = pb >= pa ? static_cast<int64_t>((pb - pa) % ld) : ld - 1 - static_cast<int64_t>((pa - pb - 1) % ld);
+  return d < a.len || ld - d < b.len;
+}
+
+wqmm_status check_memories(const Memories& m) {
+  for (int i = 0; i < m.outs; ++i) {
+    const Memory& o = m.out[i];
+    for (int j = i + 1; j < m.outs; ++j)
+      if (share(o, m.out[j])) return fail(WQMM_ERR_PARAM_INVALID, "%s shares memory with %s", o.name, m.out[j].name);
+    for (int j = 0; j < m.ins; ++j) {
+      const Memory& t = m.in[j];
+      const bool itself = t.may_be == i && t.p == o.p && t.rows == o.rows && t.len == o.len && t.ld == o.ld;
+      if (!itself && share(o, t)) return fail(WQMM_ERR_PARAM_INVALID, "%s shares memory with %s", o.name, t.name);
+    }
+  }
+  return WQMM_SUCCESS;
+}
+
+}  // namespace
+
 wqmm_status run_plan(OpKind op, void* workspace, uint64_t workspace_size, wqmm_executor* executor,
                      wqmm_stream stream) {
   wqmm_status st = take_executor(executor, op);
   if (st) return st;
   st = check_workspace(executor, workspace, workspace_size);
+  if (st == WQMM_SUCCESS) st = check_memories(executor->plan->memories);
   if (st == WQMM_SUCCESS) st = executor->plan->run(workspace, reinterpret_cast<cudaStream_t>(stream));
   release(executor);
   return st == WQMM_SUCCESS ? ok() : st;

@@ -164,6 +164,20 @@ wqmm_status check_in_place(const wqmm_tensor* in, int64_t ld_in, const wqmm_tens
   return WQMM_SUCCESS;
 }
 
+// The memory of rows of 16-bit numbers.
+Memory rows_of(const void* p, const char* name, int64_t m, int64_t len, int64_t ld, int may_be = -1) {
+  return {name, p, m, 2 * len, 2 * ld, may_be};
+}
+
+void add_weights(Memories& to, const wqmm_tensor* a, const wqmm_tensor* b, const wqmm_tensor* scale,
+                 const wqmm_tensor* offsets, const wqmm_tensor* source) {
+  to.add_in(whole(a, "loraA"));
+  to.add_in(whole(b, "loraB"));
+  if (scale) to.add_in(whole(scale, "scale"));
+  to.add_in(whole(offsets, "offsets"));
+  to.add_in(whole(source, "source"));
+}
+
 uint64_t low_bytes(const Problem& p) {
   return round_up(static_cast<uint64_t>(p.rows.m) * 2 * lora_padded_rank(p.rank) * 2, 256) +
          round_up(static_cast<uint64_t>(p.rows.m) * 4, 256);
@@ -257,6 +271,10 @@ wqmm_status add_phase1(const wqmm_tensor* x1, const wqmm_tensor* a, const wqmm_t
     if ((st = check_in_place(y, plan->y.ld, output, plan->ldo, "y"))) return st;
     plan->y.p = static_cast<const uint16_t*>(y->data);
   }
+  plan->memories.add_out(rows_of(output->data, "output", p.rows.m, p.n, plan->ldo));
+  plan->memories.add_in(rows_of(p.x.p, "x1", p.rows.m, p.k, p.x.ld, 0));
+  if (y) plan->memories.add_in(rows_of(y->data, "y", p.rows.m, p.n, plan->y.ld, 0));
+  add_weights(plan->memories, a, b, scale, offsets, source);
   plan->few = lora_one_launch(p.rows, p.rank, plan->y.p != plan->out, sm_count());
   const uint64_t workspace = plan->few ? 0 : low_bytes(p);
   return hand_out(OpKind::kLora, std::move(plan), workspace, workspace_size, executor);
@@ -307,6 +325,14 @@ wqmm_status grad_phase1(const wqmm_tensor* grad, const wqmm_tensor* x1, const wq
   }
   plan->ga = static_cast<uint16_t*>(ga->data);
   plan->gb = static_cast<uint16_t*>(gb->data);
+  if (gx) plan->memories.add_out(rows_of(gx->data, "gradX", p.rows.m, p.k, plan->ldgx));
+  plan->memories.add_out(whole(ga, "gradA"));
+  plan->memories.add_out(whole(gb, "gradB"));
+  const int first = gx ? 0 : -1;
+  plan->memories.add_in(rows_of(p.x.p, "x1", p.rows.m, p.k, p.x.ld, first));
+  plan->memories.add_in(rows_of(grad->data, "grad", p.rows.m, p.n, plan->grad.ld, first));
+  if (gx_in) plan->memories.add_in(rows_of(gx_in->data, "gradXIn", p.rows.m, p.k, plan->gx_in.ld, first));
+  add_weights(plan->memories, a, b, scale, offsets, source);
   return hand_out(OpKind::kLora, std::move(plan), 2 * low_bytes(p), workspace_size, executor);
 }
 

@@ -35,19 +35,6 @@ struct SortPlan final : OpPlan {
   }
 };
 
-int esize(int dt) {
-  switch (dt) {
-    case WQMM_DT_I8:
-    case WQMM_DT_FP8E4M3: return 1;
-    case WQMM_DT_F16:
-    case WQMM_DT_BF16: return 2;
-    case WQMM_DT_F32:
-    case WQMM_DT_I32: return 4;
-    case WQMM_DT_I64: return 8;
-    default: return 0;
-  }
-}
-
 int route_type(int dt) {
   switch (dt) {
     case WQMM_DT_F16: return kRtF16;
@@ -85,7 +72,7 @@ wqmm_status check_data(const Arg* a, int n) {
     if (!contiguous(a[i].t)) return fail(WQMM_ERR_PARAM_INVALID, "%s must be contiguous", a[i].name);
     if (numel(a[i].t) == 0) continue;
     if (!a[i].t->data) return fail(WQMM_ERR_PARAM_NULLPTR, "%s: data pointer is null", a[i].name);
-    const int es = esize(a[i].t->dtype);
+    const int es = dt_bytes(a[i].t->dtype);
     if (reinterpret_cast<uintptr_t>(a[i].t->data) % es)
       return fail(WQMM_ERR_PARAM_INVALID, "%s: data must be aligned to its elements (%d bytes)", a[i].name, es);
   }
@@ -182,7 +169,7 @@ wqmm_status dispatch_phase1(const wqmm_tensor* x, const wqmm_tensor* position, c
   const Arg args[] = {{x, "x"}, {position, "position"}, {output, "output"}};
   wqmm_status st = check_args(args, 3);
   if (st) return st;
-  const int es = esize(x->dtype);
+  const int es = dt_bytes(x->dtype);
   if (es == 0) return fail(WQMM_ERR_PARAM_INVALID, "x dtype %s cannot be dispatched", dt_name(x->dtype));
   if (output->dtype != x->dtype) return fail(WQMM_ERR_PARAM_INVALID, "output dtype must equal the x dtype");
   if (position->dtype != WQMM_DT_I32) return fail(WQMM_ERR_PARAM_INVALID, "position must be int32");
