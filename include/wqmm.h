@@ -228,7 +228,8 @@ WQMM_API wqmm_status wqmm_matmul_no_alloc(const wqmm_tensor* x1, const wqmm_tens
  * Each operator has a phase 1 of its own; route_run is the phase 2 of all.
  * Tensors are contiguous, their data aligned to their elements (16-byte
  * alignment of rows and pointers gives the full speed), and no output overlaps
- * an input.  A "slot" is one (token, choice) pair: a position tensor is (T) --
+ * an input or another output (phase 2 refuses it), but for those named below that
+ * may be the output itself.  A "slot" is one (token, choice) pair: a position tensor is (T) --
  * one choice per token -- or (T, K) or (b, s, K).  1 <= hidden <= 65535.
  *
  * route_sort_get_workspace_size -- the stable order of the slots by expert.
@@ -267,7 +268,7 @@ WQMM_API wqmm_status route_dispatch_get_workspace_size(const wqmm_tensor* x, con
  * adds nothing (its weight is not read); a token without any gets x3, or zeros.
  *  x_sorted  (rows, hidden) float16, bfloat16 or float32.
  *  weights   optional (NULL: all one), shape of position, float16, bfloat16 or float32.
- *  x3        optional addend, shape and dtype of output.
+ *  x3        optional addend, shape and dtype of output; may be the output itself.
  *  output    (T, hidden) or (b, s, hidden), dtype of x_sorted. */
 WQMM_API wqmm_status route_combine_get_workspace_size(const wqmm_tensor* x_sorted, const wqmm_tensor* position,
                                                       const wqmm_tensor* weights, const wqmm_tensor* x3,
@@ -282,7 +283,7 @@ WQMM_API wqmm_status route_combine_get_workspace_size(const wqmm_tensor* x_sorte
  * The valid entries of position are distinct; an entry outside [0, rows) gives
  * grad_weights 0, and rows no entry names keep what grad_sorted holds.
  *  grad (T, hidden) or (b, s, hidden) float16, bfloat16 or float32; x_sorted and
- *  grad_sorted (rows, hidden) of its dtype; weights and grad_weights of position's
+ *  grad_sorted (rows, hidden) of its dtype, which may be the same tensor; weights and grad_weights of position's
  *  shape, float16, bfloat16 or float32, the same dtype. */
 WQMM_API wqmm_status route_combine_grad_get_workspace_size(const wqmm_tensor* grad, const wqmm_tensor* x_sorted,
                                                            const wqmm_tensor* position, const wqmm_tensor* weights,

@@ -313,3 +313,24 @@ def test_experts_of_quantised_weights():
     half = 2.0 ** -8
     bound = size * (2 * half + (hidden + 4) * U32) * 1.02 + half * want.abs()
     assert bool(((got.cpu().double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("tokens,top,hidden", [(33, 5, 40), (130, 9, 1001), (700, 4, 2048)])
+def test_results_in_place(tokens, top, hidden):
+    """The addend as combine's result, the experts' rows as their own gradient; other sharing is refused."""
+    ids = make_ids((tokens, top), 6, drop=0.3, seed=tokens)
+    order = R.sort_tokens(ids, 6)
+    xs, x3 = randn(tokens * top, hidden, dtype=torch.bfloat16, seed=1), randn(tokens, hidden, dtype=torch.bfloat16, seed=2)
+    w = torch.rand(tokens, top, device="cuda")
+    want = R.combine_tokens(xs, order, w, x3=x3)
+    y = x3.clone()
+    assert R.combine_tokens(xs, order, w, x3=y, out=y) is y and torch.equal(y, want)
+    rows, weights = R.combine_tokens_grad(x3, xs, order, w, out=xs.clone())
+    z = xs.clone()
+    got = R.combine_tokens_grad(x3, z, order, w, out=z)
+    assert got[0] is z and torch.equal(z, rows) and torch.equal(got[1], weights)
+    for f in (lambda: R.combine_tokens(xs, order, w, out=xs[:tokens]),
+              lambda: R.combine_tokens_grad(xs[:tokens], z, order, w, out=xs),
+              lambda: R.dispatch_tokens(xs[:tokens], order, out=xs)):
+        with pytest.raises(W.WqmmError, match="shares memory"):
+            f()

@@ -146,3 +146,48 @@ def test_wrappers_refuse_host_tensors():
               lambda: routing.expert_weight_quant_matmul(x, order, [], [])):
         with pytest.raises(ValueError, match="CUDA"):
             f()
+
+
+# ------------------------------------------------------------------ memory that an output shares
+# Phase 2 refuses it before it launches; the addresses are made up, so only where no GPU could be given them.
+torch = pytest.importorskip("torch")
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses")
+BIG = 1 << 20  # apart: each tensor has a megabyte of its own
+
+TENSORS = {
+    W.route_sort_get_workspace_size: dict(ids=((6, 2), W.DT_I32), offsets=((5,), W.DT_I32),
+                                          source=((12,), W.DT_I32), position=((6, 2), W.DT_I32)),
+    W.route_dispatch_get_workspace_size: dict(x=((6, 40), W.DT_F16), position=((6, 2), W.DT_I32),
+                                              out=((12, 40), W.DT_F16)),
+    W.route_combine_get_workspace_size: dict(xs=((12, 40), W.DT_F16), position=((6, 2), W.DT_I32),
+                                             weights=((6, 2), W.DT_F32), x3=((6, 40), W.DT_F16),
+                                             out=((6, 40), W.DT_F16)),
+    W.route_combine_grad_get_workspace_size: dict(grad=((6, 40), W.DT_F16), xs=((12, 40), W.DT_F16),
+                                                  position=((6, 2), W.DT_I32), weights=((6, 2), W.DT_F32),
+                                                  gs=((12, 40), W.DT_F16), gw=((6, 2), W.DT_F32))}
+
+
+@no_gpu
+@pytest.mark.parametrize("phase1,what,at,off", [
+    (f, *v) for f, cases in {
+        W.route_sort_get_workspace_size: [("source", "ids", 0), ("position", "ids", 0), ("offsets", "ids", 44),
+                                          ("ids", "source", 44), ("position", "source", 0)],
+        W.route_dispatch_get_workspace_size: [("out", "x", 0), ("out", "x", 478), ("x", "out", 958),
+                                              ("out", "position", 0)],
+        W.route_combine_get_workspace_size: [("out", "xs", 0), ("out", "x3", 2), ("x3", "out", 478),
+                                             ("out", "weights", 0), ("out", "position", 46)],
+        W.route_combine_grad_get_workspace_size: [("gs", "grad", 0), ("gs", "xs", 2), ("gs", "weights", 0),
+                                                  ("gw", "weights", 0), ("gw", "position", 0), ("gw", "xs", 0),
+                                                  ("gs", "gw", 0)]}.items() for v in cases])
+def test_memory_in_common_is_refused(phase1, what, at, off):
+    tensors = TENSORS[phase1]
+    names = list(tensors)
+    address = {n: BIG * (i + 1) for i, n in enumerate(names)}
+    address[what] = address[at] + off
+    args = [T(*tensors[n], data=address[n]) for n in names]
+    if "ids" in tensors:
+        args.insert(1, 4)
+    st, ws, ex = phase1(*args)
+    assert st == 0, W.wqmm_last_error()
+    assert W.route_run(BIG * 64, ws, ex, 0) == INVALID
+    assert "shares memory" in W.wqmm_last_error()

@@ -157,7 +157,10 @@ wqmm_status sort_phase1(const wqmm_tensor* ids, int64_t groups, const wqmm_tenso
   p.source = static_cast<int*>(source->data);
   p.position = static_cast<int*>(position->data);
   const uint64_t ws = round_up(plan_sort(p), 256);
-  return hand_out(OpKind::kRoute, std::make_unique<SortPlan>(p), ws, workspace_size, executor);
+  auto plan = std::make_unique<SortPlan>(p);
+  for (int i = 1; i < 4; ++i) plan->memories.add_out(whole(args[i].t, args[i].name));
+  plan->memories.add_in(whole(ids, "expertIds"));
+  return hand_out(OpKind::kRoute, std::move(plan), ws, workspace_size, executor);
 }
 
 wqmm_status dispatch_phase1(const wqmm_tensor* x, const wqmm_tensor* position, const wqmm_tensor* output,
@@ -195,8 +198,11 @@ wqmm_status dispatch_phase1(const wqmm_tensor* x, const wqmm_tensor* position, c
   p.rows = output->shape[0];
   p.row_bytes = hidden * es;
   p.top = static_cast<int>(top);
-  using Plan = RoutePlan<DispatchParams, launch_dispatch>;
-  return hand_out(OpKind::kRoute, std::make_unique<Plan>(p, "token dispatch launch"), 0, workspace_size, executor);
+  auto plan = std::make_unique<RoutePlan<DispatchParams, launch_dispatch>>(p, "token dispatch launch");
+  plan->memories.add_out(whole(output, "output"));
+  plan->memories.add_in(whole(x, "x"));
+  plan->memories.add_in(whole(position, "position"));
+  return hand_out(OpKind::kRoute, std::move(plan), 0, workspace_size, executor);
 }
 
 wqmm_status combine_phase1(const wqmm_tensor* x_sorted, const wqmm_tensor* position, const wqmm_tensor* weights,
@@ -246,8 +252,13 @@ wqmm_status combine_phase1(const wqmm_tensor* x_sorted, const wqmm_tensor* posit
   p.top = static_cast<int>(top);
   p.type = route_type(x_sorted->dtype);
   p.wtype = weights ? route_type(weights->dtype) : kRtF32;
-  using Plan = RoutePlan<CombineParams, launch_combine>;
-  return hand_out(OpKind::kRoute, std::make_unique<Plan>(p, "token combine launch"), 0, workspace_size, executor);
+  auto plan = std::make_unique<RoutePlan<CombineParams, launch_combine>>(p, "token combine launch");
+  plan->memories.add_out(whole(output, "output"));
+  plan->memories.add_in(whole(x_sorted, "xSorted"));
+  plan->memories.add_in(whole(position, "position"));
+  if (weights) plan->memories.add_in(whole(weights, "weights"));
+  if (x3) plan->memories.add_in(whole(x3, "x3", 0));
+  return hand_out(OpKind::kRoute, std::move(plan), 0, workspace_size, executor);
 }
 
 wqmm_status combine_grad_phase1(const wqmm_tensor* grad, const wqmm_tensor* x_sorted, const wqmm_tensor* position,
@@ -303,9 +314,15 @@ wqmm_status combine_grad_phase1(const wqmm_tensor* grad, const wqmm_tensor* x_so
   p.top = static_cast<int>(top);
   p.type = route_type(grad->dtype);
   p.wtype = route_type(weights->dtype);
-  using Plan = RoutePlan<CombineGradParams, launch_combine_grad>;
-  return hand_out(OpKind::kRoute, std::make_unique<Plan>(p, "token combine gradient launch"), 0, workspace_size,
-                  executor);
+  auto plan =
+      std::make_unique<RoutePlan<CombineGradParams, launch_combine_grad>>(p, "token combine gradient launch");
+  plan->memories.add_out(whole(grad_sorted, "gradSorted"));
+  plan->memories.add_out(whole(grad_weights, "gradWeights"));
+  plan->memories.add_in(whole(grad, "grad"));
+  plan->memories.add_in(whole(x_sorted, "xSorted", 0));
+  plan->memories.add_in(whole(position, "position"));
+  plan->memories.add_in(whole(weights, "weights"));
+  return hand_out(OpKind::kRoute, std::move(plan), 0, workspace_size, executor);
 }
 
 }  // namespace
