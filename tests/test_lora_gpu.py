@@ -505,3 +505,23 @@ def test_columns_of_one_matrix(rows, rank):
     with pytest.raises(W.WqmmError, match="shares memory"):
         lora.lora_grad(y, x, c.a, c.b, c.order, c.scale, grad_x=wide[:, 184:280], in_place=True)
     assert torch.equal(wide, now)
+
+
+def test_raw_handle_of_the_default_stream():
+    """Its handle is 0: the call runs there, behind what is already on it."""
+    c = Case(300, 256, 128, 16, 3, "bf16")
+    want = lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=c.y)
+    assert torch.cuda.default_stream().cuda_stream == 0
+    with W._on_stream(0, c.x.get_device()):
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    y = torch.zeros_like(c.y)
+    torch.cuda._sleep(100_000_000)  # 50 ms
+    y.copy_(c.y)
+    got = lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=y, stream=0)
+    assert torch.equal(got, want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # the handle names the stream, whichever is current
+        got = lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=y, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)

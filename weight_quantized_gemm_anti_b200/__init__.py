@@ -372,7 +372,8 @@ def _on_stream(stream, device=None):
     `device` (None: the current one), so that what the call allocates belongs to that stream."""
     import torch
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        # 0 is the default stream's handle, but no address of an external one
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
     elif device is not None and stream.device_index != device:
         raise ValueError(f"the stream is on device {stream.device_index}, the tensors on {device}")
     return torch.cuda.stream(stream)  # makes its device current too
