@@ -525,3 +525,19 @@ def test_raw_handle_of_the_default_stream():
         got = lora.lora_add(c.x, c.a, c.b, c.order, c.scale, y=y, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_order_of_indexes_that_are_copied_first():
+    """One index per request, for its rows: not contiguous, so the call makes a copy, on the given stream too."""
+    old, new = torch.zeros(30, 1, dtype=torch.int32, device="cuda"), torch.arange(30, dtype=torch.int32, device="cuda")[:, None]
+    ids = old.clone()
+    side = torch.cuda.Stream()
+    lora.adapter_order(ids.expand(30, 17), 30, stream=side)  # the kernels are loaded: nothing else waits below
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # 50 ms
+        ids.copy_(new)
+    got = lora.adapter_order(ids.expand(30, 17), 30, stream=side)
+    side.synchronize()
+    want = lora.adapter_order(new.expand(30, 17).reshape(-1), 30)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))

@@ -22,7 +22,10 @@ from .routing import TokenOrder, sort_tokens
 def adapter_order(adapter_ids, num_adapters: int, stream=None) -> TokenOrder:
     """The rows in the order of their adapters: adapter_ids (m), one index per row, int32 or int64; an index outside
     [0, num_adapters) is a row without adapter.  For x1 of (b, s, k) the rows are counted through."""
-    return sort_tokens(adapter_ids.reshape(-1), num_adapters, stream)
+    if stream is not None:
+        with _on_stream(stream, _same_device(adapter_ids)):  # where a copy that reshape makes belongs too
+            return adapter_order(adapter_ids, num_adapters)
+    return sort_tokens(adapter_ids.reshape(-1), num_adapters)
 
 
 def lora_add(x1, lora_a, lora_b, order: TokenOrder, scale=None, y=None, out=None, stream=None):
