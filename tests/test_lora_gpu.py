@@ -541,3 +541,24 @@ def test_order_of_indexes_that_are_copied_first():
     side.synchronize()
     want = lora.adapter_order(new.expand(30, 17).reshape(-1), 30)
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_projection_refuses_before_it_writes():
+    m, k = 40, 128
+    c = Case(m, k, k, 16, 4, "bf16")
+    q = torch.randint(-128, 128, (k, k), dtype=torch.int8, generator=torch.Generator().manual_seed(1)).cuda()
+    s = torch.full((k,), 0.002, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(c.y, 3)
+    half = TokenOrder(c.order.offsets, c.order.source[:m // 2], None)
+    for args in ((c.a.float(), c.b, c.order), (c.a[:, :12], c.b, c.order), (c.a, c.b[:2], c.order), (c.a, c.b, half),
+                 (c.a.cpu(), c.b, c.order), (c.a, c.b, c.order, c.scale.cpu())):
+        with pytest.raises((W.WqmmError, ValueError)):
+            lora.lora_weight_quant_matmul(c.x, W.desc(q), s, *args, out=out)
+        assert bool((out == 3).all())
+    # the adapters read x1 after the projection has written its result
+    x = c.x.clone()
+    with pytest.raises(ValueError, match="shares memory"):
+        lora.lora_weight_quant_matmul(x, W.desc(q), s, c.a, c.b, c.order, out=x)
+    assert torch.equal(x, c.x)
+    got = lora.lora_weight_quant_matmul(c.x, W.desc(q), s, c.a, c.b, c.order, c.scale, out=out)
+    assert got is out and torch.equal(out, lora.lora_weight_quant_matmul(c.x, W.desc(q), s, c.a, c.b, c.order, c.scale))

@@ -367,6 +367,14 @@ def _same_device(*tensors) -> int:
     return dev
 
 
+def _share_memory(a, b) -> bool:
+    """Whether two contiguous tensors have a byte in common."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    pa, pb = a.data_ptr(), b.data_ptr()
+    return pa < pb + b.numel() * b.element_size() and pb < pa + a.numel() * a.element_size()
+
+
 def _on_stream(stream, device=None):
     """The context in which an operator allocates and launches on `stream`, a torch.cuda.Stream or a raw handle of
     `device` (None: the current one), so that what the call allocates belongs to that stream."""

@@ -15,7 +15,8 @@ from __future__ import annotations
 
 import torch
 
-from . import _on_stream, _same_device, binding, weight_quant_matmul
+from . import (_on_stream, _same_device, _share_memory, binding, check, desc, lora_get_workspace_size,
+               weight_quant_matmul, wqmm_executor_destroy)
 from .routing import TokenOrder, sort_tokens
 
 
@@ -43,12 +44,23 @@ def lora_weight_quant_matmul(x1, x2_desc, antiquant_scale, lora_a, lora_b, order
                              stream=None):
     """The anti-quant projection of x1 with the rows' adapters added in place:
     out = x1 @ ((x2 + antiquant_offset) * antiquant_scale) + bias + x3 + the adapters' part.  The projection is
-    rounded to the output type before the adapters' part is added, and the sum once more."""
-    device = _same_device(x1, antiquant_scale, antiquant_offset, bias, x3, out)
+    rounded to the output type before the adapters' part is added, and the sum once more.  ``out`` may not share
+    memory with x1, which the adapters read behind the projection."""
+    device = _same_device(x1, antiquant_scale, antiquant_offset, bias, x3, out, lora_a, lora_b, order.offsets,
+                          order.source, lora_scale)
     if stream is not None or device != torch.cuda.current_device():
         with torch.cuda.device(device) if stream is None else _on_stream(stream, device):
             return lora_weight_quant_matmul(x1, x2_desc, antiquant_scale, lora_a, lora_b, order, lora_scale,
                                             antiquant_offset, bias, x3, antiquant_group_size, out)
+    if out is not None:
+        # the adapters' arguments are refused before the projection has written the caller's tensor
+        if _share_memory(out, x1):
+            raise ValueError("out shares memory with x1")
+        status, _, executor = lora_get_workspace_size(
+            *(None if t is None else desc(t) for t in (x1, lora_a, lora_b, lora_scale, order.offsets, order.source,
+                                                       out, out)))
+        check(status)
+        wqmm_executor_destroy(executor)
     out = weight_quant_matmul(x1, x2_desc, antiquant_scale, antiquant_offset, bias, x3, antiquant_group_size, out)
     return lora_add(x1, lora_a, lora_b, order, lora_scale, y=out, out=out)
 
