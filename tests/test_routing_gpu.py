@@ -334,3 +334,24 @@ def test_results_in_place(tokens, top, hidden):
               lambda: R.dispatch_tokens(xs[:tokens], order, out=xs)):
         with pytest.raises(W.WqmmError, match="shares memory"):
             f()
+
+
+def expert_case(tokens=37, top=2, hidden=128, n=64, experts=5):
+    ids = make_ids((tokens, top), experts, drop=0.1)
+    order = R.sort_tokens(ids, experts)
+    rows = R.dispatch_tokens(randn(tokens, hidden, dtype=torch.bfloat16), order)
+    qs = [torch.randint(-128, 128, (hidden, n), dtype=torch.int8, generator=torch.Generator().manual_seed(e)).cuda()
+          for e in range(experts)]
+    scales = [torch.full((n,), 0.002 * (e + 1), dtype=torch.bfloat16, device="cuda") for e in range(experts)]
+    return order, rows, qs, [W.desc(q) for q in qs], scales
+
+
+@pytest.mark.parametrize("kept", [0, 1, 20, 50, 74])
+def test_experts_of_fewer_rows_than_slots(kept):
+    """Rows up to a capacity: what lies behind is dropped, whole experts among it."""
+    order, rows, _, descs, scales = expert_case()
+    want = R.expert_weight_quant_matmul(rows, order, descs, scales)
+    end = min(kept, int(order.offsets[-1]))
+    for bounds in (None, order.offsets.tolist()):
+        got = R.expert_weight_quant_matmul(rows[:kept], order, descs, scales, bounds=bounds)
+        assert tuple(got.shape) == (kept, 64) and torch.equal(got[:end], want[:end])

@@ -74,8 +74,8 @@ def expert_weight_quant_matmul(x_sorted, order: TokenOrder, x2_descs: Sequence, 
                                antiquant_group_size: int = 0, out=None, bounds: Optional[Sequence[int]] = None,
                                stream=None):
     """out[rows of e] = the anti-quant GEMM of expert e's rows of x_sorted with its weight, for every expert that
-    has rows.  ``bounds``: order.offsets on the host (None: read here, which waits for the stream).  Rows behind
-    the last expert keep what ``out`` holds."""
+    has rows.  ``bounds``: order.offsets on the host (None: read here, which waits for the stream).  An x_sorted of
+    fewer rows than slots has no rows for what lies behind.  Rows behind the last expert keep what ``out`` holds."""
     device = _same_device(x_sorted, out)
     if stream is not None or device != torch.cuda.current_device():
         with torch.cuda.device(device) if stream is None else _on_stream(stream, device):
@@ -85,6 +85,7 @@ def expert_weight_quant_matmul(x_sorted, order: TokenOrder, x2_descs: Sequence, 
         bounds = order.offsets.tolist()
     if len(bounds) != len(x2_descs) + 1:
         raise ValueError(f"{len(x2_descs)} weights for {len(bounds) - 1} experts")
+    bounds = [min(b, x_sorted.shape[0]) for b in bounds]
     if out is None:
         out = x_sorted.new_empty((x_sorted.shape[0], x2_descs[0].shape[1]))
     for e, desc in enumerate(x2_descs):
