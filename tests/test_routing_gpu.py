@@ -346,6 +346,27 @@ def expert_case(tokens=37, top=2, hidden=128, n=64, experts=5):
     return order, rows, qs, [W.desc(q) for q in qs], scales
 
 
+def test_experts_refuse():
+    order, rows, qs, descs, scales = expert_case()
+    out = torch.full((rows.shape[0], 64), 3.0, device="cuda").bfloat16()
+    bounds = order.offsets.tolist()
+    down = [bounds[0], bounds[2], bounds[1], *bounds[3:]]
+    for kw in (dict(x2_descs=[]), dict(x2_descs=descs[:4]), dict(antiquant_scales=scales[:4]),
+               dict(antiquant_scales=scales + scales[:1]), dict(antiquant_offsets=scales[:2]), dict(biases=scales[:3]),
+               dict(bounds=bounds[:-1]), dict(bounds=[0]), dict(bounds=down), dict(bounds=[-1, *bounds[1:]]),
+               dict(out=out[:bounds[-1] - 1]), dict(out=out[0]), dict(x_sorted=rows.view(2, -1, 128))):
+        with pytest.raises(ValueError):
+            R.expert_weight_quant_matmul(**{**dict(x_sorted=rows, order=order, x2_descs=descs,
+                                                   antiquant_scales=scales, out=out, bounds=bounds), **kw})
+        assert bool((out == 3).all()), kw
+    square = [torch.randint(-128, 128, (128, 128), dtype=torch.int8, device="cuda") for _ in qs]
+    wide = [torch.full((128,), 0.002, dtype=torch.bfloat16, device="cuda") for _ in qs]
+    before = rows.clone()
+    with pytest.raises(ValueError, match="shares memory"):
+        R.expert_weight_quant_matmul(rows, order, [W.desc(q) for q in square], wide, out=rows)
+    assert torch.equal(rows.view(torch.int16), before.view(torch.int16))  # as bits: rows of no slot hold anything
+
+
 @pytest.mark.parametrize("kept", [0, 1, 20, 50, 74])
 def test_experts_of_fewer_rows_than_slots(kept):
     """Rows up to a capacity: what lies behind is dropped, whole experts among it."""

@@ -20,7 +20,7 @@ from typing import NamedTuple, Optional, Sequence
 
 import torch
 
-from . import _on_stream, _same_device, binding, weight_quant_matmul
+from . import _on_stream, _same_device, _share_memory, binding, weight_quant_matmul
 
 
 class TokenOrder(NamedTuple):
@@ -74,24 +74,41 @@ def expert_weight_quant_matmul(x_sorted, order: TokenOrder, x2_descs: Sequence, 
                                antiquant_group_size: int = 0, out=None, bounds: Optional[Sequence[int]] = None,
                                stream=None):
     """out[rows of e] = the anti-quant GEMM of expert e's rows of x_sorted with its weight, for every expert that
-    has rows.  ``bounds``: order.offsets on the host (None: read here, which waits for the stream).  An x_sorted of
-    fewer rows than slots has no rows for what lies behind.  Rows behind the last expert keep what ``out`` holds."""
+    has rows.  The lists have one entry per expert (a bias, offset or, for weights that are not quantised, scale may
+    be None).  ``bounds``: order.offsets on the host (None: read here, which waits for the stream).  An x_sorted of
+    fewer rows than slots has no rows for what lies behind.  Rows behind the last expert keep what ``out`` holds;
+    ``out`` may not share memory with x_sorted."""
     device = _same_device(x_sorted, out)
     if stream is not None or device != torch.cuda.current_device():
         with torch.cuda.device(device) if stream is None else _on_stream(stream, device):
             return expert_weight_quant_matmul(x_sorted, order, x2_descs, antiquant_scales, antiquant_offsets, biases,
                                               antiquant_group_size, out, bounds)
+    if len(x2_descs) == 0:
+        raise ValueError("no experts")
+    for name, entries in (("antiquant_scales", antiquant_scales), ("antiquant_offsets", antiquant_offsets),
+                          ("biases", biases)):
+        if entries is not None and len(entries) != len(x2_descs):
+            raise ValueError(f"{len(entries)} {name} for {len(x2_descs)} weights")
+    if x_sorted.dim() != 2:
+        raise ValueError(f"x_sorted must be 2-D (rows, hidden), got {x_sorted.dim()}-D")
     if bounds is None:
         bounds = order.offsets.tolist()
     if len(bounds) != len(x2_descs) + 1:
         raise ValueError(f"{len(x2_descs)} weights for {len(bounds) - 1} experts")
+    if bounds[0] < 0 or any(lo > hi for lo, hi in zip(bounds, bounds[1:])):
+        raise ValueError("bounds must ascend from 0 or more")
     bounds = [min(b, x_sorted.shape[0]) for b in bounds]
+    if out is not None:
+        if out.dim() != 2 or out.shape[0] < bounds[-1]:
+            raise ValueError(f"out must be 2-D with {bounds[-1]} rows or more, got {tuple(out.shape)}")
+        if _share_memory(out, x_sorted):
+            raise ValueError("out shares memory with x_sorted")
     if out is None:
         out = x_sorted.new_empty((x_sorted.shape[0], x2_descs[0].shape[1]))
     for e, desc in enumerate(x2_descs):
         lo, hi = bounds[e], bounds[e + 1]
         if lo < hi:
-            weight_quant_matmul(x_sorted[lo:hi], desc, antiquant_scales[e],
+            weight_quant_matmul(x_sorted[lo:hi], desc, None if antiquant_scales is None else antiquant_scales[e],
                                 None if antiquant_offsets is None else antiquant_offsets[e],
                                 None if biases is None else biases[e],
                                 antiquant_group_size=antiquant_group_size, out=out[lo:hi])
