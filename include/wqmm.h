@@ -324,7 +324,7 @@ WQMM_API wqmm_status lora_get_workspace_size(const wqmm_tensor* x1, const wqmm_t
  *     grad_x[r] = grad_x_in[r] + scale[a] * (grad[r] @ lora_b[a]) @ lora_a[a]
  *     grad_a[a] = scale[a] * sum_r (grad[r] @ lora_b[a])^T x1[r]
  *     grad_b[a] = scale[a] * sum_r grad[r]^T (x1[r] @ lora_a[a]^T)     over the rows r of adapter a
- *  grad       (m, n) or (b, s, n); grad_x optional (NULL: not wanted) and
+ *  m <= 2^24.  grad  (m, n) or (b, s, n); grad_x optional (NULL: not wanted) and
  *  grad_x_in  optional addend (the projection's own part; may be grad_x itself),
  *             (m, k) or (b, s, k), all of x1's dtype, row strides as above.  grad_x may
  *             also be x1 or, where k = n, grad (and grad_x_in with it: a residual's

@@ -192,3 +192,13 @@ GRAD_SQUARE = dict(grad=((6, 64), BF16), b=((3, 64, 16), BF16), gb=((3, 64, 16),
 def test_grad_refuses_memory_in_common(at, kw):
     assert run_at(W.lora_grad_get_workspace_size, list(GRAD), GRAD, at, **kw) == INVALID
     assert "shares memory" in W.wqmm_last_error()
+
+
+def test_rows_of_the_gradients():
+    """One CTA may go through all rows of an adapter while others wait, for a bounded time: fewer rows than forward."""
+    rows = lambda m: {n: ((m, GRAD[n][0][1]), BF16) for n in ("grad", "x1", "gx_in", "gx")} | dict(source=((m,), I32))
+    assert grad(**rows(2 ** 24))[0] == 0
+    assert grad(**rows(2 ** 24 + 1))[0] == INVALID and "rows" in W.wqmm_last_error()
+    assert grad(**rows(2 ** 26))[0] == INVALID
+    assert add(x1=((2 ** 26, 64), BF16), source=((2 ** 26,), I32), y=None, out=((2 ** 26, 96), BF16))[0] == 0
+    assert add(x1=((2 ** 26 + 1, 64), BF16), source=((2 ** 26 + 1,), I32), y=None, out=((2 ** 26 + 1, 96), BF16))[0] == INVALID

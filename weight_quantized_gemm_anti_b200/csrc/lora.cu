@@ -12,9 +12,12 @@ using namespace wqmm;
 namespace {
 
 constexpr int64_t kMaxRank = 128;
-// Row numbers and the next tile's stay within 32 bits, and one CTA goes through all rows of an adapter in well
-// under the two seconds that a kernel waits for another role.
+// Row numbers and the next tile's stay within 32 bits.
 constexpr int64_t kMaxRows = 1 << 26;
+// In the weights' gradients one CTA may have all rows of an adapter (few items of many adapters), and the warps that
+// write its sums wait for it, two seconds at most.  A step of 64 rows copies 48 KB at the largest rank: 2^22 rows of
+// float16 at rank 128 (all of one of 100 adapters, k = n = 32) take 90 ms, so these 0.36 s, a fifth of the limit.
+constexpr int64_t kMaxGradRows = 1 << 24;
 
 struct Arg {
   const wqmm_tensor* t;
@@ -299,6 +302,9 @@ wqmm_status grad_phase1(const wqmm_tensor* grad, const wqmm_tensor* x1, const wq
   auto plan = std::make_unique<GradPlan>();
   if ((st = check_problem(x1, a, b, scale, offsets, source, &plan->p))) return st;
   const Problem& p = plan->p;
+  if (p.rows.m > kMaxGradRows)
+    return fail(WQMM_ERR_PARAM_INVALID, "x1: %lld rows, the gradients take at most %lld", (long long)p.rows.m,
+                (long long)kMaxGradRows);
   if ((st = check_like(grad, "grad", p.rows.m, p.n, &plan->grad.ld))) return st;
   plan->grad.p = static_cast<const uint16_t*>(grad->data);
   plan->gx = nullptr;
