@@ -2,6 +2,7 @@
 binding of the routing and adapter operators, _binding.so."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -29,15 +30,30 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _newest_input() -> float:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "wqmm.h"), __file__]
-    return max(os.path.getmtime(f) for f in files)
+def _older(built: str, inputs) -> bool:
+    """Whether `built` is missing or older than one of its inputs."""
+    return not os.path.exists(built) or any(os.path.getmtime(f) > os.path.getmtime(built) for f in inputs)
+
+
+def _inputs(binding: bool) -> list:
+    """What the binding, or the library, is built from."""
+    own = [f for f in os.listdir(CSRC) if (f == "binding.cpp") == binding]
+    return [*(os.path.join(CSRC, f) for f in own), os.path.join(ROOT, "include", "wqmm.h"), __file__]
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    newest = _newest_input()
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest for f in (LIB, BINDING)):
-        return LIB
+    """Build what is not up to date.  The library needs nvcc alone; the binding also needs torch, and without it
+    there is none."""
+    if force or _older(LIB, _inputs(False)):
+        build_library(verbose, extra)
+    if importlib.util.find_spec("torch") is None:
+        print("torch is not installed: no binding of the routing and adapter operators is built", file=sys.stderr)
+    elif force or _older(BINDING, _inputs(True)):
+        build_binding(verbose)
+    return LIB
+
+
+def build_library(verbose: bool = False, extra=()) -> str:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     cc = nvcc()
@@ -55,7 +71,6 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     tmp = LIB + ".tmp"
     subprocess.run([cc, *ARCH, "-shared", "-Xlinker", "-soname=libwqmm.so", "-o", tmp, *objs, "-Xcompiler", "-fPIC"], check=True)
     os.replace(tmp, LIB)
-    build_binding(verbose)
     return LIB
 
 
