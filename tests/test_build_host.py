@@ -63,6 +63,20 @@ def test_a_source_of_the_library(compiled):
     assert "libwqmm.so" in compiled and "api.o" in compiled
 
 
+@pytest.mark.parametrize("what", ["torch", "python"])
+def test_another_torch_or_python(compiled, monkeypatch, what):
+    """The binding is built for one interpreter and one torch: under another it is built anew."""
+    torch = pytest.importorskip("torch")
+    if what == "torch":
+        monkeypatch.setattr(torch, "__version__", "9.9.9")
+    else:
+        monkeypatch.setattr(buildlib.sysconfig, "get_config_var", lambda name: "cpython-999")
+    buildlib.build()
+    assert compiled == ["_binding.so"]
+    buildlib.build()
+    assert compiled == ["_binding.so"]
+
+
 def test_without_torch(compiled, monkeypatch, capsys):
     """The library needs nvcc alone; there is no binding then, and build() says so."""
     find = importlib.util.find_spec

@@ -14,7 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libwqmm.so")
-BINDING = os.path.join(HERE, "_binding.so")
+BINDING = os.path.join(HERE, "_binding.so")  # beside it _binding.so.abi: what it was built for
 SOURCES = ["api.cu", "kernels_aux.cu", "kernels_wqmm.cu", "kernels_smallm.cu", "kernels_qmm.cu", "noalloc.cu",
            "route.cu", "kernels_route.cu", "lora.cu", "lora_few.cu", "lora_shrink.cu", "lora_expand.cu",
            "lora_outer.cu"]
@@ -41,6 +41,21 @@ def _inputs(binding: bool) -> list:
     return [*(os.path.join(CSRC, f) for f in own), os.path.join(ROOT, "include", "wqmm.h"), __file__]
 
 
+def _abi() -> str:
+    """What a binding is built for: this interpreter and this torch."""
+    import torch
+    return f"{sysconfig.get_config_var('SOABI')} torch {torch.__version__} cxx11abi {torch._C._GLIBCXX_USE_CXX11_ABI}"
+
+
+def _binding_abi() -> str:
+    """What the binding that is there was built for."""
+    try:
+        with open(BINDING + ".abi") as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Build what is not up to date.  The library needs nvcc alone; the binding also needs torch, and without it
     there is none."""
@@ -48,7 +63,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         build_library(verbose, extra)
     if importlib.util.find_spec("torch") is None:
         print("torch is not installed: no binding of the routing and adapter operators is built", file=sys.stderr)
-    elif force or _older(BINDING, _inputs(True)):
+    elif force or _older(BINDING, _inputs(True)) or _binding_abi() != _abi():
         build_binding(verbose)
     return LIB
 
@@ -91,6 +106,8 @@ def build_binding(verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
+    with open(BINDING + ".abi", "w") as f:
+        f.write(_abi())
     return BINDING
 
 
