@@ -202,3 +202,13 @@ def test_rows_of_the_gradients():
     assert grad(**rows(2 ** 26))[0] == INVALID
     assert add(x1=((2 ** 26, 64), BF16), source=((2 ** 26,), I32), y=None, out=((2 ** 26, 96), BF16))[0] == 0
     assert add(x1=((2 ** 26 + 1, 64), BF16), source=((2 ** 26 + 1,), I32), y=None, out=((2 ** 26 + 1, 96), BF16))[0] == INVALID
+
+
+def test_flags_without_a_truth_value():
+    """The error of a flag's own truth value is what the caller gets."""
+    x, a, b = torch.zeros(6, 64), torch.zeros(3, 16, 64), torch.zeros(3, 96, 16)
+    i = torch.zeros(6, dtype=torch.int32)
+    both = torch.tensor([True, False])
+    for need, in_place in ((both, False), (True, both)):
+        with pytest.raises(RuntimeError, match="Boolean value"):
+            W.binding().lora_grad(torch.zeros(6, 96), x, a, b, None, i, i, x, need, in_place)

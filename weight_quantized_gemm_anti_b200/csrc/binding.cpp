@@ -56,6 +56,12 @@ const at::Tensor* tensor(PyObject* o, bool optional = false) {
   return &THPVariable_Unpack(o);
 }
 
+bool truth(PyObject* o) {
+  const int t = PyObject_IsTrue(o);
+  if (t < 0) throw Failed();
+  return t == 1;
+}
+
 struct Desc {
   wqmm_tensor d{};
   const wqmm_tensor* p = nullptr;
@@ -237,7 +243,7 @@ PyObject* lora_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor *grad = tensor(a[0]), *x = tensor(a[1]), *la = tensor(a[2]), *lb = tensor(a[3]),
                    *scale = tensor(a[4], true), *offsets = tensor(a[5]), *source = tensor(a[6]),
                    *gx_in = tensor(a[7], true);
-  const bool need = PyObject_IsTrue(a[8]) == 1, in_place = PyObject_IsTrue(a[9]) == 1;
+  const bool need = truth(a[8]), in_place = truth(a[9]);
   OnDevice on({grad, x, la, lb, scale, offsets, source, gx_in});
   at::Tensor gx, ga = make(la->sizes(), *la), gb = make(lb->sizes(), *lb);
   if (need) gx = in_place && gx_in ? *gx_in : make(x->sizes(), *x);
