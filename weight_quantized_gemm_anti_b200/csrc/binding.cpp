@@ -237,6 +237,20 @@ PyObject* lora_add(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END
 }
 
+// (x1, lora_a, lora_b, scale, offsets, source, y, out) -> None: what lora_add would refuse of its arguments is refused
+PyObject* check_lora_add(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BEGIN count(n, 8);
+  const at::Tensor *x = tensor(a[0]), *la = tensor(a[1]), *lb = tensor(a[2]), *scale = tensor(a[3], true),
+                   *offsets = tensor(a[4]), *source = tensor(a[5]), *y = tensor(a[6], true), *out = tensor(a[7]);
+  uint64_t size = 0;
+  wqmm_executor* ex = nullptr;
+  check(lora_get_workspace_size(Desc(x), Desc(la), Desc(lb), Desc(scale), Desc(offsets), Desc(source), Desc(y),
+                                Desc(out), &size, &ex));
+  wqmm_executor_destroy(ex);
+  Py_RETURN_NONE;
+  END
+}
+
 // (grad, x1, lora_a, lora_b, scale, offsets, source, grad_x_in, need_grad_x, in_place) -> (grad_x, grad_a, grad_b)
 PyObject* lora_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   BEGIN count(n, 10);
@@ -260,8 +274,8 @@ PyObject* lora_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {METHOD(sort_tokens),         METHOD(dispatch_tokens), METHOD(combine_tokens),
-                           METHOD(combine_tokens_grad), METHOD(lora_add),        METHOD(lora_grad),
-                           {nullptr, nullptr, 0, nullptr}};
+                           METHOD(combine_tokens_grad), METHOD(lora_add),        METHOD(check_lora_add),
+                           METHOD(lora_grad),           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods};
 
 }  // namespace

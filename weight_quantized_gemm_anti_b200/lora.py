@@ -15,8 +15,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (_on_stream, _same_device, _share_memory, binding, check, desc, lora_get_workspace_size,
-               weight_quant_matmul, wqmm_executor_destroy)
+from . import _on_stream, _same_device, _share_memory, binding, weight_quant_matmul
 from .routing import TokenOrder, sort_tokens
 
 
@@ -56,11 +55,7 @@ def lora_weight_quant_matmul(x1, x2_desc, antiquant_scale, lora_a, lora_b, order
         # the adapters' arguments are refused before the projection has written the caller's tensor
         if _share_memory(out, x1):
             raise ValueError("out shares memory with x1")
-        status, _, executor = lora_get_workspace_size(
-            *(None if t is None else desc(t) for t in (x1, lora_a, lora_b, lora_scale, order.offsets, order.source,
-                                                       out, out)))
-        check(status)
-        wqmm_executor_destroy(executor)
+        binding().check_lora_add(x1, lora_a, lora_b, lora_scale, order.offsets, order.source, out, out)
     out = weight_quant_matmul(x1, x2_desc, antiquant_scale, antiquant_offset, bias, x3, antiquant_group_size, out)
     return lora_add(x1, lora_a, lora_b, order, lora_scale, y=out, out=out)
 
