@@ -36,6 +36,8 @@ namespace wqmm {
 namespace {
 
 constexpr int kThreads = 128;
+// The power of two of a float16 row of low that has no finite value but zero: below those of all others.
+constexpr float kNoValue = 0x1p-127f;
 
 // ------------------------------------------------------------------ types
 template <bool BF16>

@@ -8,15 +8,16 @@ namespace {
 
 // Four neighbours of a row of low (LANES lanes have the row) times `scale`, as
 // two 16-bit numbers each.  float16: the row is first brought to where its
-// largest finite value is below 2^15 by a power of two, whose inverse is returned.  A row of zeros
-// (a masked token's) takes the largest power: its inverse must not be the largest of its adapter's rows,
-// to which the weights' gradients bring them all.  Values that are not finite stay so under any power;
-// beside them the row's others keep their bits.
+// largest finite value is below 2^15 by a power of two, whose inverse is returned.  A row without one
+// (a masked token's zeros) returns kNoValue: its factor must not be the largest of its adapter's rows, to
+// which the weights' gradients bring them all.  Values that are not finite stay so under any power; beside
+// them the row's others keep their bits.
 template <bool BF16, int LANES>
 __device__ __forceinline__ float split_row(float (&v)[4], float scale, uint2& hi, uint2& lo) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] *= scale;
   float up = 1.f;
+  bool has = true;
   if constexpr (!BF16) {
     // the row's largest value, NaN and infinities aside
     float top = 0.f;
@@ -24,6 +25,7 @@ __device__ __forceinline__ float split_row(float (&v)[4], float scale, uint2& hi
     for (int i = 0; i < 4; ++i) top = fmaxf(top, isfinite(v[i]) ? fabsf(v[i]) : 0.f);
 #pragma unroll
     for (int d = 1; d < LANES; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    has = top > 0.f;
     // 2^14 <= top * up < 2^15: the exponent's complement, within the normal numbers
     const int e = static_cast<int>(__float_as_uint(top) >> 23);
     up = __uint_as_float(static_cast<uint32_t>(min(268 - e, 253)) << 23);
@@ -40,7 +42,7 @@ __device__ __forceinline__ float split_row(float (&v)[4], float scale, uint2& hi
   }
   hi = make_uint2(h[0], h[1]);
   lo = make_uint2(l[0], l[1]);
-  return __uint_as_float((254u << 23) - __float_as_uint(up));  // 1 / up, exactly
+  return has ? __uint_as_float((254u << 23) - __float_as_uint(up)) : kNoValue;  // 1 / up, exactly
 }
 
 // Four neighbours of the sum of NW warps' parts, `stride` floats apart.

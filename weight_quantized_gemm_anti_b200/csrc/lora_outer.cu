@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
   __shared__ __align__(8) uint64_t full[S], empty[S], sums_full[2], sums_empty[2], top_ready[2], done;
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
-  __shared__ float top_sh[2], tops[4];
+  __shared__ float top_sh[2], tops[4], leasts[4];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -159,24 +159,40 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
           has ? (o.which == 0 ? p0 : p1).low.factor[o.begin + i * 64 + ((tid & 127) + j * kCopyThreads) / (4 * RT)] : 0.f;
     }
   };
+  // The rows' powers of two beside the largest are exact in 16 bits down to 2^-24.  (A row of kNoValue has nothing
+  // but zeros, infinities and NaN: any power but zero will do.)
   auto store_low = [&](int st, float below) {
 #pragma unroll
     for (int j = 0; j < (BF16 ? 0 : kLowChunks); ++j) {
-      // the row's power of two beside the largest: exact in 16 bits down to 2^-24, below it multiplies in 32 (the
-      // least of them keeps an infinity's product one); either way each number is rounded once
-      const float ratio = fmaxf(held_by[j] * below, 0x1p-126f);
-      const __half2 by = __float2half2_rn(ratio);
+      const __half2 by = __float2half2_rn(fmaxf(held_by[j] * below, 0x1p-24f));
       uint32_t w[4] = {held[j].x, held[j].y, held[j].z, held[j].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const __half2 u = *reinterpret_cast<const __half2*>(&w[k]);
-        __half2 v;
-        if (ratio >= 0x1p-24f) {
-          v = __hmul2(u, by);
-        } else {
-          const float2 f = __half22float2(u);
-          v = __floats2half2_rn(f.x * ratio, f.y * ratio);
-        }
+        const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&w[k]), by);
+        w[k] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      *reinterpret_cast<uint4*>(sm + low_to(st, j)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  };
+  // An item with rows further apart: multiplied in 32 bits, each number rounded once.  From memory again and not
+  // unrolled, since it is rare: unrolled beside the above it took a tenth of the gradients' time at rank 128.
+  auto store_far = [&](const Item& o, int i, int st, float below) {
+#pragma unroll 1
+    for (int j = 0; j < (BF16 ? 0 : kLowChunks); ++j) {
+      bool has;
+      const uint16_t* from = low_from(o, i, j, has);
+      uint4 u = make_uint4(0, 0, 0, 0);
+      float by = 0.f;
+      if (has) {
+        u = *reinterpret_cast<const uint4*>(from);
+        by = fmaxf((o.which == 0 ? p0 : p1).low.factor[o.begin + i * 64 + ((tid & 127) + j * kCopyThreads) / (4 * RT)] * below,
+                   0x1p-126f);
+      }
+      uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        const __half2 v = __floats2half2_rn(f.x * by, f.y * by);
         w[k] = *reinterpret_cast<const uint32_t*>(&v);
       }
       *reinterpret_cast<uint4*>(sm + low_to(st, j)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -224,18 +240,28 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
     for (int it = first; it < items; it += stride, ++k) {
       const Item o = item_at(it);
       float below = 1.f;
+      bool far = false;
       if constexpr (!BF16) {
-        // the largest power of two of this CTA's rows
+        // the largest power of two of this CTA's rows, and the smallest (kNoValue aside)
         const float* factor = (o.which == 0 ? p0 : p1).low.factor + o.begin;
         const int n = min(o.n * 64, o.r1 - o.begin);
-        float top = 0.f;
-        for (int r = t; r < n; r += kCopyThreads) top = fmaxf(top, factor[r]);
+        float top = 0.f, least = 0x1p127f;
+        for (int r = t; r < n; r += kCopyThreads) {
+          const float f = factor[r];
+          top = fmaxf(top, f);
+          least = fminf(least, f > kNoValue ? f : 0x1p127f);
+        }
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-        named_bar_sync(1, kCopyThreads);  // the last item's maxima are read
-        if (lane == 0) tops[warp & 3] = top;
+        for (int s = 16; s > 0; s >>= 1) {
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+          least = fminf(least, __shfl_xor_sync(0xffffffffu, least, s));
+        }
+        named_bar_sync(1, kCopyThreads);  // the last item's are read
+        if (lane == 0) tops[warp & 3] = top, leasts[warp & 3] = least;
         named_bar_sync(1, kCopyThreads);
         top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        least = fminf(fminf(leasts[0], leasts[1]), fminf(leasts[2], leasts[3]));
+        far = least < top * 0x1p-24f;
         if (!(top > 0.f)) top = 1.f;  // no rows
         below = 1.f / top;            // of a power of two: exact
         // the maximum of two items ago has been read when its sums have
@@ -253,7 +279,10 @@ __global__ void __launch_bounds__(kOuterThreads) outer_tc_kernel(LoraRows rows, 
         if constexpr (BF16) {
           copy_low(o, i, st);
         } else {
-          store_low(st, below);
+          if (far)
+            store_far(o, i, st, below);
+          else
+            store_low(st, below);
           load_low(o, i + 1);
         }
         hand_over(&full[st]);
