@@ -136,8 +136,12 @@ def test_wrappers_refuse():
 
 # ------------------------------------------------------------------ memory that an output shares
 # Phase 2 refuses it before it launches; the addresses are made up, so only where no GPU could be given them.
-torch = pytest.importorskip("torch")
-no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses")
+try:
+    import torch
+    NO_GPU = not torch.cuda.is_available()
+except ImportError:
+    NO_GPU = True
+no_gpu = pytest.mark.skipif(not NO_GPU, reason="made-up addresses")
 BIG = 1 << 20  # apart: each tensor has a megabyte of its own
 
 
@@ -206,6 +210,7 @@ def test_rows_of_the_gradients():
 
 def test_flags_without_a_truth_value():
     """The error of a flag's own truth value is what the caller gets."""
+    torch = pytest.importorskip("torch")
     x, a, b = torch.zeros(6, 64), torch.zeros(3, 16, 64), torch.zeros(3, 96, 16)
     i = torch.zeros(6, dtype=torch.int32)
     both = torch.tensor([True, False])

@@ -9,7 +9,7 @@ projection's weight is frozen).
 
 Every call works on the tensors' device and on its current stream, or on
 ``stream`` (a torch.cuda.Stream or a raw handle; the caller orders the inputs
-before it), and does not wait for the GPU.
+before it and keeps them until it has run), and does not wait for the GPU.
 """
 from __future__ import annotations
 
@@ -31,7 +31,7 @@ def adapter_order(adapter_ids, num_adapters: int, stream=None) -> TokenOrder:
 def lora_add(x1, lora_a, lora_b, order: TokenOrder, scale=None, y=None, out=None, stream=None):
     """out[r] = y[r] + scale[a] * (x1[r] @ lora_a[a].T) @ lora_b[a].T, a the adapter of row r; a row without adapter
     gets y, or zeros.  x1 (m, k) or (b, s, k); lora_a (adapters, rank, k); lora_b (adapters, n, rank); scale
-    (adapters) float32; ``out`` may be ``y``, and ``x1`` where k = n."""
+    (adapters) float32; ``out`` may be ``y``, and ``x1`` where k = n, and shares no other memory with them."""
     if stream is not None:
         with _on_stream(stream, _same_device(x1, lora_a, lora_b, order.offsets, order.source, scale, y, out)):
             return lora_add(x1, lora_a, lora_b, order, scale, y, out)
@@ -65,7 +65,7 @@ def lora_grad(grad, x1, lora_a, lora_b, order: TokenOrder, scale=None, grad_x=No
     """The gradients of ``lora_add`` given ``grad`` of its result (y's is ``grad`` itself): (for x1, lora_a, lora_b).
     ``grad_x`` (m, k): what else x1's gradient has, the projection's own part, added in 32 bits before the one
     rounding; with ``in_place`` the sum goes into that tensor (which may be ``grad`` itself where k = n, or ``x1``).
-    ``need_grad_x`` False: None in x1's place."""
+    ``need_grad_x`` False: None in x1's place.  At most 2^24 rows."""
     if stream is not None:
         with _on_stream(stream, _same_device(grad, x1, lora_a, lora_b, order.offsets, order.source, scale, grad_x)):
             return lora_grad(grad, x1, lora_a, lora_b, order, scale, grad_x, need_grad_x, in_place)

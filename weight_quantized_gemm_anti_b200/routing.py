@@ -11,8 +11,8 @@ adapters of ``lora`` read.
 
 Every call works on the tensors' device and on its current stream, or on
 ``stream`` (a torch.cuda.Stream or a raw handle; the caller orders the inputs
-before it).  No call waits for the GPU except ``expert_weight_quant_matmul``
-without ``bounds``.
+before it and keeps them until it has run).  No call waits for the GPU except
+``expert_weight_quant_matmul`` without ``bounds``.
 """
 from __future__ import annotations
 
@@ -52,7 +52,7 @@ def dispatch_tokens(x, order: TokenOrder, out=None, stream=None):
 def combine_tokens(x_sorted, order: TokenOrder, weights=None, x3=None, out=None, stream=None):
     """out[t] = x3[t] + sum_j weights[t, j] * x_sorted[position[t, j]], in 32 bits, rounded once.  ``weights``:
     shape of position, float16, bfloat16 or float32; None: all one, which is also the gradient of
-    ``dispatch_tokens``.  ``out``: (T, hidden) unless x3 or ``out`` says (b, s, hidden)."""
+    ``dispatch_tokens``.  ``out``: (T, hidden) unless x3 or ``out`` says (b, s, hidden); it may be x3 itself."""
     if stream is not None:
         with _on_stream(stream, _same_device(x_sorted, order.position, weights, x3, out)):
             return combine_tokens(x_sorted, order, weights, x3, out)
@@ -61,8 +61,8 @@ def combine_tokens(x_sorted, order: TokenOrder, weights=None, x3=None, out=None,
 
 def combine_tokens_grad(grad, x_sorted, order: TokenOrder, weights, out=None, stream=None):
     """The gradient of ``combine_tokens`` for x_sorted and weights, given ``grad`` of its result:
-    (grad_sorted, grad_weights).  Rows of no slot keep what ``out`` (grad_sorted's tensor, made here unless given)
-    holds; grad_weights of a slot of no expert is 0."""
+    (grad_sorted, grad_weights).  Rows of no slot keep what ``out`` (grad_sorted's tensor) holds (in an ``out`` made
+    here that is uninitialised memory); it may be x_sorted itself.  grad_weights of a slot of no expert is 0."""
     if stream is not None:
         with _on_stream(stream, _same_device(grad, x_sorted, order.position, weights, out)):
             return combine_tokens_grad(grad, x_sorted, order, weights, out)
